@@ -1,0 +1,378 @@
+"""Cases of the grouped products by expert, their gradients, the block quantiser and the fp8 block products.
+
+With ``own`` false every operator is computed in its plain form (elementary torch operations in 32 bits,
+rounded once at the end); with ``own`` true through the library's entry points.
+
+Row matrices hold the pairs (token, chosen expert) sorted by expert.  ``align`` 0 packs the experts' runs
+tightly; 16 or 128 starts every run at a multiple of that many rows, as ``moe_align`` lays them out, and the
+rows between the runs are nobody's: they keep the zeros that the output buffers start with.
+"""
+import numpy as np
+import torch
+
+own = False
+
+FP8 = torch.float8_e4m3fn
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------------------------------- cases
+
+def _grouped(name, op, T, k, E, N, K, skew, align, out, layout="rows"):
+    c = dict(op=op, T=T, k=k, E=E, N=N, K=K, skew=skew, align=align, out=out, layout=layout)
+    return dict(c, name=name) if name else c
+
+
+def _dense(name, M, N, K, out, layout="rows"):
+    c = dict(op="block_mm", M=M, N=N, K=K, out=out, layout=layout)
+    return dict(c, name=name) if name else c
+
+
+def _quantize(name, M, K):
+    c = dict(op="quantize", M=M, K=K)
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # one token's eight experts, gate_up of a bf16 bank: latency and weight streaming
+        _grouped("mm one token", "mm", 1, 8, 256, 1024, 2048, 1.0, 0, "bf16"),
+        # a decode batch's down projection, two rows an expert on average
+        _grouped("mm decode", "mm", 64, 8, 256, 2048, 512, 1.0, 0, "f32"),
+        # a prefill batch's gate_up, uneven experts
+        _grouped("mm prefill", "mm", 8192, 8, 256, 1024, 2048, 1.0, 0, "bf16"),
+        # gradients of a small layer with sizes off every tile
+        _grouped("grad small", "grad", 101, 2, 8, 264, 200, 0.5, 0, "f32"),
+        # gradients of a layer of many small experts, ragged runs
+        _grouped("grad many experts", "grad", 4096, 8, 256, 1024, 2048, 0.7, 0, "bf16"),
+        # gradients of a layer of few large experts
+        _grouped("grad few experts", "grad", 8192, 2, 8, 4096, 4096, 0.3, 0, "f32"),
+        # one token's activations before an fp8 product
+        _quantize("quantize one token", 1, 2048),
+        # a prefill batch's pairs between the two expert products
+        _quantize("quantize prefill", 65536, 2048),
+        # one token through a shared expert's gate_up
+        _dense("block mm one token", 1, 1024, 2048, "f32"),
+        # a prefill batch through a dense projection
+        _dense("block mm prefill", 8192, 4096, 4096, "bf16"),
+        # a decode batch over a packed fp8 bank, runs as the alignment lays them out
+        _grouped("grouped block mm decode", "grouped_block_mm", 64, 8, 256, 1024, 2048, 1.0, 16, "bf16", "tile16"),
+        # a prefill batch over an fp8 bank in the checkpoint's order
+        _grouped("grouped block mm prefill", "grouped_block_mm", 4096, 8, 256, 1024, 2048, 1.0, 0, "bf16"),
+    ]
+
+
+def _log(rng, lo, hi, step=1):
+    """A size in [lo, hi], spread over its logarithm, a multiple of `step`."""
+    v = int(round(lo * (hi / lo) ** rng.random()))
+    return min(hi, max(lo, v // step * step))
+
+
+def draw(rng):
+    op = rng.choice(["mm", "grad", "quantize", "block_mm", "grouped_block_mm"])
+    if op == "quantize":
+        while True:
+            M, K = _log(rng, 1, 65536), _log(rng, 16, 8192, 16)
+            if M * K <= 65536 * 2048:
+                return _quantize(None, M, K)
+    if op == "block_mm":
+        layout = rng.choice(["rows", "tile16"])
+        while True:
+            M, N, K = _log(rng, 1, 8192), _log(rng, 64, 8192, 16 if layout == "tile16" else 1), _log(rng, 128, 8192, 16)
+            if M * N * K <= 8192 * 4096 * 4096:
+                return _dense(None, M, N, K, rng.choice(["bf16", "f32"]), layout)
+    fp8 = op == "grouped_block_mm"
+    layout = rng.choice(["rows", "tile16"]) if fp8 else "rows"
+    while True:
+        E = rng.choice([4, 8, 16, 32, 60, 64, 128, 160, 256])
+        k, T = rng.choice([1, 2, 4, 6, 8]), _log(rng, 1, 8192)
+        N = _log(rng, 64, 4096, 16 if layout == "tile16" else 1 if fp8 else 8)
+        K = _log(rng, 64, 4096, 16 if fp8 else 8)
+        if k <= E and T * k * N * K <= 65536 * 1024 * 2048 and E * N * K <= 128 * 1024 * 2048:
+            return _grouped(None, op, T, k, E, N, K, rng.choice([0.0, 0.5, 1.0]), rng.choice([0, 0, 16, 128]),
+                            rng.choice(["bf16", "f32"]), layout)
+
+
+def _counts(c, rng):
+    """Rows of each expert when T tokens choose k different experts each, some experts liked more."""
+    like = rng.standard_normal(c["E"]) * c["skew"]
+    score = like + rng.gumbel(size=(c["T"], c["E"]))
+    ids = np.argpartition(-score, c["k"] - 1, axis=1)[:, :c["k"]] if c["k"] < c["E"] else np.tile(np.arange(c["E"]), (c["T"], 1))
+    return np.bincount(ids.ravel(), minlength=c["E"])
+
+
+def _offsets(c, counts):
+    """The runs' starts, and the rows of the row matrices: enough for any routing."""
+    step = c["align"] or 1
+    room = (c["T"] * c["k"] + c["E"] * (step - 1) + step - 1) // step * step
+    return np.concatenate([[0], np.cumsum((counts + step - 1) // step * step)]), room
+
+
+# ------------------------------------------------------------------------------------------- inputs
+
+def _activations(g, M, K):
+    """bf16 rows of N(0, 1) with every 61st channel eight times as large."""
+    x = torch.randn(M, K, device="cuda", generator=g)
+    x[:, 7::61] *= 8
+    return x.to(torch.bfloat16)
+
+
+def _codes_of_rows(x):
+    """e4m3 codes and block-major scales of bf16 rows (inputs of the fp8 products)."""
+    M, K = x.shape
+    KB = -(-K // 128)
+    xb = torch.zeros(M, KB * 128, device="cuda")
+    xb[:, :K] = x
+    xb = xb.view(M, KB, 128)
+    s = (xb.abs().amax(2).double() / 448).float()
+    q = (xb / s.clamp_min(1e-30)[:, :, None]).view(M, KB * 128)[:, :K].to(FP8).contiguous()
+    return q, s.t().contiguous()
+
+
+def _fp8_weights(g, E, N, K):
+    """e4m3 codes [E, N, K] that use the format's whole range and a scale for each 128 x 128 block."""
+    q = torch.empty(E, N, K, dtype=FP8, device="cuda")
+    for e in range(E):
+        q[e] = (torch.randn(N, K, device="cuda", generator=g) * 100).clamp(-448, 448).to(FP8)
+    s = torch.rand(E, -(-N // 128), -(-K // 128), device="cuda", generator=g) * 2e-4 + 1e-4
+    return q, s
+
+
+def _tile16(q):
+    """Codes [E, N, K] in the banks' packed order: 16-row tiles, each stored as its 16-byte pieces column by column."""
+    E, N, K = q.shape
+    b = q.view(torch.uint8).view(E, N // 16, 16, K // 16, 16).permute(0, 1, 3, 2, 4)
+    return b.contiguous().view(E, N, K).view(FP8)
+
+
+def _rows(q):
+    """The inverse of _tile16."""
+    E, N, K = q.shape
+    b = q.view(torch.uint8).view(E, N // 16, K // 16, 16, 16).permute(0, 1, 3, 2, 4)
+    return b.contiguous().view(E, N, K).view(FP8)
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    s = {"op": c["op"], "dtype": DTYPES.get(c.get("out"))}
+    if c["op"] == "quantize":
+        s["x"] = _activations(g, c["M"], c["K"])
+        s["q"] = torch.empty(c["M"], c["K"], dtype=FP8, device="cuda")
+        s["scale"] = torch.empty(-(-c["K"] // 128), c["M"], device="cuda")
+        return s
+    if c["op"] == "block_mm":
+        M, N, K = c["M"], c["N"], c["K"]
+        s["xq"], s["xs"] = _codes_of_rows(_activations(g, M, K))
+        w, ws = _fp8_weights(g, 1, N, K)
+        s["layout"] = c["layout"]
+        s["w"], s["ws"] = (_tile16(w) if c["layout"] == "tile16" else w)[0], ws[0]
+        s["y"] = torch.zeros(M, N, dtype=s["dtype"], device="cuda")
+        return s
+    E, N, K = c["E"], c["N"], c["K"]
+    counts = _counts(c, rng)
+    offsets, M = _offsets(c, counts)
+    s["rows"], s["most"] = int(counts.sum()), int(counts.max())
+    s["offsets"] = torch.from_numpy(offsets.astype(np.int32)).cuda()
+    s["counts"] = torch.from_numpy(counts.astype(np.int32)).cuda()
+    if c["op"] == "grouped_block_mm":
+        s["xq"], s["xs"] = _codes_of_rows(_activations(g, M, K))
+        w, s["ws"] = _fp8_weights(g, E, N, K)
+        s["layout"] = c["layout"]
+        s["w"] = _tile16(w) if c["layout"] == "tile16" else w
+    else:
+        s["x"] = _activations(g, M, K)
+        s["w"] = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+        for e in range(E):
+            s["w"][e] = torch.randn(N, K, device="cuda", generator=g) * 0.02
+    if c["op"] == "grad":
+        s["dy"] = torch.randn(M, N, device="cuda", generator=g).to(torch.bfloat16)
+        s["dx"] = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        s["dw"] = torch.zeros(E, N, K, dtype=s["dtype"], device="cuda")
+    else:
+        s["y"] = torch.zeros(M, N, dtype=s["dtype"], device="cuda")
+    return s
+
+
+# ------------------------------------------------------------------------------------------- plain forms
+
+def _places(s):
+    """For every row of some expert: the row, its expert, its place in the expert's run."""
+    starts, counts = s["offsets"][:-1].long(), s["counts"].long()
+    slot = torch.arange(s["rows"], device="cuda")
+    first = torch.cumsum(counts, 0) - counts
+    e = torch.repeat_interleave(torch.arange(len(counts), device="cuda"), counts, output_size=s["rows"])
+    place = slot - first[e]
+    return starts[e] + place, e, place
+
+
+def _spread(s, x, at):
+    """Rows as [E, most, width] in 32 bits, zeros after each run."""
+    r, e, place = at
+    z = torch.zeros(s["counts"].numel(), s["most"], x.shape[1], device="cuda")
+    z[e, place] = x[r].float()
+    return z
+
+
+def _gather(z, at, M, dtype):
+    """Back to the row matrix, rows of nobody zero."""
+    r, e, place = at
+    y = torch.zeros(M, z.shape[2], dtype=dtype, device="cuda")
+    y[r] = z[e, place].to(dtype)
+    return y
+
+
+def _by_block(s, n, width):
+    """Block scales [.., nb, kb] spread to [.., n, width]."""
+    return s.repeat_interleave(128, -2)[..., :n, :].repeat_interleave(128, -1)[..., :width]
+
+
+def _plain_mm(s):
+    at = _places(s)
+    z = torch.bmm(_spread(s, s["x"], at), s["w"].float().transpose(1, 2).contiguous())
+    return _gather(z, at, s["x"].shape[0], s["dtype"])
+
+
+def _plain_grad(s):
+    at = _places(s)
+    dy = _spread(s, s["dy"], at)
+    dx = _gather(torch.bmm(dy, s["w"].float()), at, s["dy"].shape[0], torch.bfloat16)
+    dw = torch.bmm(dy.transpose(1, 2).contiguous(), _spread(s, s["x"], at)).to(s["dtype"])
+    return dx, dw
+
+
+def _plain_quantize(s):
+    M, K = s["x"].shape
+    KB = -(-K // 128)
+    x = torch.nn.functional.pad(s["x"].float(), (0, KB * 128 - K)).view(M, KB, 128)
+    scale = (x.abs().amax(2).double() / 448).float()  # 64 bits: a division by a number may be a product with 1 / 448
+    q = (x.double() / torch.where(scale > 0, scale, torch.ones_like(scale)).double()[:, :, None]).float()  # ties matter
+    return q.view(M, KB * 128)[:, :K].to(FP8), scale.t().contiguous()
+
+
+def _plain_block_mm(s):
+    (M, K), N = s["xq"].shape, s["w"].shape[0]
+    w = _rows(s["w"][None])[0] if s["layout"] == "tile16" else s["w"]
+    x = s["xq"].float() * s["xs"].t().repeat_interleave(128, 1)[:, :K]
+    return torch.mm(x, (w.float() * _by_block(s["ws"], N, K)).t()).to(s["dtype"])
+
+
+def _plain_grouped_block_mm(s):
+    at = _places(s)
+    (M, K), N = s["xq"].shape, s["w"].shape[1]
+    w = _rows(s["w"]) if s["layout"] == "tile16" else s["w"]
+    x = s["xq"].float() * s["xs"].t().repeat_interleave(128, 1)[:, :K]
+    w = w.float().mul_(_by_block(s["ws"], N, K))
+    z = torch.bmm(_spread(s, x, at), w.transpose(1, 2).contiguous())
+    return _gather(z, at, M, s["dtype"])
+
+
+PLAIN = {"mm": _plain_mm, "grad": _plain_grad, "quantize": _plain_quantize, "block_mm": _plain_block_mm,
+         "grouped_block_mm": _plain_grouped_block_mm}
+
+
+def run(state):
+    s = state
+    if not own:
+        return PLAIN[s["op"]](s)
+    import quantized_moe_expert_topk_amd as qm
+    if s["op"] == "quantize":
+        return qm.moe_quantize_blocks(s["x"], s["q"], s["scale"])
+    if s["op"] == "mm":
+        return qm.moe_grouped_mm(s["x"], s["w"], s["offsets"], s["counts"], s["rows"], out=s["y"])
+    if s["op"] == "grad":
+        return (qm.moe_grouped_mm_dgrad(s["dy"], s["w"], s["offsets"], s["counts"], s["rows"], out=s["dx"]),
+                qm.moe_grouped_mm_wgrad(s["dy"], s["x"], s["offsets"], s["counts"], s["rows"], out=s["dw"]))
+    layout = qm.MOE_LAYOUT_TILE16 if s["layout"] == "tile16" else qm.MOE_LAYOUT_ROWS
+    if s["op"] == "block_mm":
+        return qm.moe_block_mm(s["xq"], s["xs"], s["w"], s["ws"], layout=layout, out=s["y"])
+    return qm.moe_grouped_block_mm(s["xq"], s["xs"], s["w"], s["ws"], s["offsets"], s["counts"], s["rows"],
+                                   layout=layout, out=s["y"])
+
+
+# ------------------------------------------------------------------------------------------- work
+
+def work(case):
+    c = case
+    if c["op"] == "quantize":
+        M, K = c["M"], c["K"]
+        return {"bytes": 3 * M * K + 4 * M * -(-K // 128), "flops": 3 * M * K}
+    out = 2 if c["out"] == "bf16" else 4
+    N, K = c["N"], c["K"]
+    NB, KB = -(-N // 128), -(-K // 128)
+    if c["op"] == "block_mm":
+        M = c["M"]
+        return {"bytes": M * K + 4 * M * KB + N * K + 4 * NB * KB + out * M * N, "flops": 2 * M * N * K}
+    R, E = c["T"] * c["k"], c["E"]
+    active = int(np.count_nonzero(_counts(c, np.random.default_rng(0))))  # weights of idle experts are not needed
+    if c["op"] == "grouped_block_mm":
+        return {"bytes": R * K + 4 * R * KB + active * (N * K + 4 * NB * KB) + out * R * N + 8 * E, "flops": 2 * R * N * K}
+    if c["op"] == "mm":
+        return {"bytes": 2 * R * K + 2 * active * N * K + out * R * N + 8 * E, "flops": 2 * R * N * K}
+    return {"bytes": 2 * R * N + 2 * R * K + 2 * active * N * K + 2 * R * K + out * E * N * K + 8 * E,
+            "flops": 4 * R * N * K}
+
+
+# ------------------------------------------------------------------------------------------- 64 bits
+
+def _e4m3_grid(v):
+    """The e4m3 value nearest to each number of |v| <= 448, ties to the even one."""
+    m, e = torch.frexp(v.abs())
+    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp_min(-6) - 3)
+    return torch.round(v / step) * step
+
+
+def _dequant(q, scale_rows):
+    """Codes [n, K] times scales [n, blocks of 128]."""
+    n, K = q.shape
+    KB = scale_rows.shape[1]
+    z = torch.zeros(n, KB * 128, dtype=torch.float64, device="cuda")
+    z[:, :K] = q.to(torch.float32).double()
+    return (z.view(n, KB, 128) * scale_rows.double()[:, :, None]).view(n, KB * 128)[:, :K]
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    if c["op"] == "quantize":
+        x = s["x"].double()
+        M, K = x.shape
+        q, scale = torch.zeros_like(x), torch.zeros_like(s["scale"], dtype=torch.float64)
+        for b in range(scale.shape[0]):
+            part = x[:, 128 * b:128 * b + 128]
+            unit = (part.abs().max(1).values / 448).float().double()  # the scale is a float32, and so is each quotient
+            scale[b] = unit
+            quotient = (part / torch.where(unit > 0, unit, torch.ones_like(unit))[:, None]).float().double()
+            q[:, 128 * b:128 * b + 128] = _e4m3_grid(quotient)
+        return q, scale
+    if c["op"] == "block_mm":
+        w = s["w"]
+        if c["layout"] == "tile16":
+            N, K = w.shape
+            w = w.view(torch.uint8).reshape(N // 16, K // 16, 16, 16).transpose(1, 2).reshape(N, K).view(FP8)
+        x = _dequant(s["xq"], s["xs"].t())
+        w = _dequant(w, s["ws"][torch.arange(c["N"], device="cuda") // 128])
+        return x @ w.t()
+    starts, counts = s["offsets"].tolist(), s["counts"].tolist()
+    M = s["x" if "x" in s else "xq"].shape[0]
+    if c["op"] == "grad":
+        dx = torch.zeros(M, c["K"], dtype=torch.float64, device="cuda")
+        dw = torch.zeros(c["E"], c["N"], c["K"], dtype=torch.float64, device="cuda")
+        for e in range(c["E"]):
+            rows = slice(starts[e], starts[e] + counts[e])
+            dy = s["dy"][rows].double()
+            dx[rows] = dy @ s["w"][e].double()
+            dw[e] = dy.t() @ s["x"][rows].double()
+        return dx, dw
+    y = torch.zeros(M, c["N"], dtype=torch.float64, device="cuda")
+    for e in range(c["E"]):
+        rows = slice(starts[e], starts[e] + counts[e])
+        if c["op"] == "mm":
+            y[rows] = s["x"][rows].double() @ s["w"][e].double().t()
+            continue
+        w = s["w"][e]
+        if c["layout"] == "tile16":
+            w = w.view(torch.uint8).reshape(c["N"] // 16, c["K"] // 16, 16, 16).transpose(1, 2).reshape(c["N"], c["K"]).view(FP8)
+        w = _dequant(w, s["ws"][e][torch.arange(c["N"], device="cuda") // 128])
+        y[rows] = _dequant(s["xq"][rows], s["xs"][:, rows].t()) @ w.t()
+    return y
