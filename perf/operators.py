@@ -319,7 +319,7 @@ def work(case):
 def _e4m3_grid(v):
     """The e4m3 value nearest to each number of |v| <= 448, ties to the even one."""
     m, e = torch.frexp(v.abs())
-    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp_min(-6) - 3)
+    step = ((e.long() - 1).clamp_min(-6) - 3 + 1023 << 52).view(torch.float64)  # a power of two, made of its bits
     return torch.round(v / step) * step
 
 
