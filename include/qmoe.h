@@ -355,6 +355,79 @@ int moe_layer_forward(const void *x_bf16, int T, const void *w_router_bf16, cons
                       void *out, int out_dtype, void *route_workspace, size_t route_workspace_bytes,
                       void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------ grouped products
+ *
+ * Products of row matrices with one weight matrix per expert, over ragged row ranges: the
+ * plain form of the expert layer's GEMMs, for projections the fused layer does not have, and
+ * their gradients, for training the experts.
+ *   offsets, counts  int32 device arrays.  The rows of expert e are
+ *                [offsets[e], offsets[e] + counts[e]) with counts [E], or
+ *                [offsets[e], offsets[e + 1]) with counts NULL and offsets [E + 1].  moe_align's
+ *                offsets and counts are in this form (its padding rows are then nobody's).
+ *                Any range may be empty; ranges must not overlap.  A range is cut to [0, M), so
+ *                no device value makes a call read or write outside its matrices; with
+ *                overlapping ranges the outputs are undefined.
+ *   M            rows of the row matrices.  Rows of no expert are neither read nor written.
+ *   expected_rows  about how many rows the experts hold together (T*k), 0 if unknown (M).  It only
+ *                picks the kernel; any value >= 0 gives a valid result.
+ * Sums are fp32 in a fixed order: results do not vary from call to call.  Values in rows of no
+ * expert never reach another row; a NaN or infinity in a row of an expert reaches that row's
+ * outputs (forward, dgrad) or that expert's gradient (wgrad) only.
+ * Requires 1 <= E <= 1024, N and K multiples of 8 and at most 4 million, and 16-byte aligned
+ * matrices; an output must not overlap an operand. */
+
+/* y[r, n] = sum_k x[r, k] w[e, n, k] for every row r of expert e.
+ *   x_bf16 [M, K], w_bf16 [E, N, K] row-major; y [M, N] f32 or bf16 (out_dtype MOE_OUT_*). */
+int moe_grouped_mm(const void *x_bf16, const void *w_bf16, const int32_t *offsets,
+                   const int32_t *counts, int E, int M, int expected_rows, int N, int K, void *y,
+                   int out_dtype, void *stream);
+
+/* The gradient with respect to x: dx[r, k] = sum_n dy[r, n] w[e, n, k] for every row r of expert e.
+ *   dy_bf16 [M, N], w_bf16 [E, N, K]; dx [M, K] f32 or bf16. */
+int moe_grouped_mm_dgrad(const void *dy_bf16, const void *w_bf16, const int32_t *offsets,
+                         const int32_t *counts, int E, int M, int expected_rows, int N, int K,
+                         void *dx, int out_dtype, void *stream);
+
+/* The gradient with respect to w: dw[e, n, k] = sum over the rows r of expert e of
+ * dy[r, n] x[r, k]; zeros for an expert without rows.
+ *   dy_bf16 [M, N], x_bf16 [M, K]; dw [E, N, K] f32 or bf16, every element written.
+ *   accumulate != 0 (f32 only) adds to dw instead, for gradients summed over micro-batches. */
+int moe_grouped_mm_wgrad(const void *dy_bf16, const void *x_bf16, const int32_t *offsets,
+                         const int32_t *counts, int E, int M, int expected_rows, int N, int K,
+                         void *dw, int out_dtype, int accumulate, void *stream);
+
+/* ------------------------------------------------------------------ fp8 block products
+ *
+ * Products of e4m3 activations and e4m3 weights (W8A8), both with fp32 scales: activations one
+ * per row and 128 consecutive k, weights one per 128 x 128 block (MOE_FMT_FP8_BLOCK128).  The
+ * expert layer multiplies such banks with bf16 activations; these multiply in fp8, at twice the
+ * matrix rate and half the activation bytes. */
+
+/* moe_quantize_blocks -- bf16 rows to e4m3 codes and block scales:
+ *   scale[b, r] = max |x[r, k]| / 448 over the k of block b = k / 128 (the last one may be short)
+ *   q[r, k]     = e4m3(x[r, k] / scale[b, r]), both divisions and the conversion rounded to
+ *                 nearest even; a block of zeros has scale 0 and codes 0.
+ * A NaN in a block makes its scale NaN and all its codes NaN; an infinity makes the scale
+ * infinite, its own code NaN and the others 0 (so the block's products are NaN).
+ *   x_bf16 [M, K]; q e4m3 bytes [M, K]; scale f32 [ceil(K / 128), M] (block-major: the scales that
+ *   a tile of rows needs for one block are adjacent).  K a multiple of 16. */
+int moe_quantize_blocks(const void *x_bf16, int M, int K, void *q, float *scale, void *stream);
+
+/* y[r, n] = sum_b xs[b, r] ws[n / 128, b] sum_{k in block b} xq[r, k] wq[n, k]
+ *   xq e4m3 [M, K], xs f32 [ceil(K / 128), M] (moe_quantize_blocks); wq e4m3 [N, K], ws f32
+ *   [ceil(N / 128), ceil(K / 128)]; y [M, N] f32 or bf16.
+ *   layout  MOE_LAYOUT_ROWS, or MOE_LAYOUT_TILE16 for the weight codes of a packed bank (then N a
+ *           multiple of 16).  Any N >= 1 otherwise; K a multiple of 16. */
+int moe_block_mm(const void *xq, const float *xs, const void *wq, const float *ws, int layout,
+                 int M, int N, int K, void *y, int out_dtype, void *stream);
+
+/* The same by expert: wq [E, N, K], ws [E, ceil(N / 128), ceil(K / 128)] (an FP8_BLOCK128 bank's
+ * gate_up and gate_up_scale with N = 2I and K = H, or its down and down_scale with N = H and
+ * K = I); row ranges, expected_rows and rows of no expert as for the grouped products. */
+int moe_grouped_block_mm(const void *xq, const float *xs, const void *wq, const float *ws, int layout,
+                         const int32_t *offsets, const int32_t *counts, int E, int M,
+                         int expected_rows, int N, int K, void *y, int out_dtype, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 const char *moe_status_string(int status); /* static text for a status code */

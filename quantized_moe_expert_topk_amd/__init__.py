@@ -11,3 +11,5 @@ from .api import (AlignOut, DeviceBank, MoeLayer, alloc_align, choose_block_m, m
                   moe_expert_gate_up, moe_layer_forward, moe_pack_bank, moe_route, moe_route_align,
                   moe_route_align_workspace_bytes,
                   moe_route_from_logits, moe_route_workspace_bytes, moe_workspace_bytes)
+from .grouped import (moe_block_mm, moe_grouped_block_mm, moe_grouped_mm, moe_grouped_mm_dgrad,  # noqa: F401
+                      moe_grouped_mm_wgrad, moe_quantize_blocks)

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <string>
 
+#include "abi_common.h"
 #include "launch.h"
 #include "qmoe.h"
 
@@ -440,6 +441,22 @@ int forward_workspace_need(const moe_bank *routed, const moe_bank *shared, const
   *need = p.total;
   return MOE_OK;
 }
+
+}  // namespace qmoe
+
+namespace qmoe {
+
+int abi_fail(int code, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(code, "%s", buf);
+}
+int abi_ok() { return ok(); }
+int abi_check_device() { return check_device(); }
+int abi_hip_status(hipError_t e, const char *what) { return hip_status(e, what); }
 
 }  // namespace qmoe
 

@@ -123,4 +123,32 @@ hipError_t launch_act_mx8(const uint16_t *x, int rows, int K, uint8_t *q, uint8_
 hipError_t launch_combine(const void *Y, bool y_bf16, const float *topk_w, int T, int k, int H, int has_shared,
                           void *out, int out_bf16, hipStream_t s);
 
+// ---- grouped products by expert and fp8 block products (grouped_mm.hip, block_mm.hip)
+
+// The rows of expert e are [offsets[e], offsets[e] + counts[e]), or up to offsets[e + 1] where
+// counts is NULL.  Device values are not trusted: the kernels cut every range to [0, M).
+struct Groups {
+  const int32_t *offsets, *counts;  // offsets NULL: one expert that has all M rows
+  int E, M;
+};
+
+constexpr int kForward = 0, kDgrad = 1, kWgrad = 2;
+
+struct ProductArgs {
+  const uint8_t *x;   // forward: x rows; the gradients: dy rows
+  const uint8_t *w;   // forward, dgrad: the weights; wgrad: x rows
+  const float *xs, *ws;  // fp8: activation scales [KB, M], weight scales [E, NB, KB]
+  void *out;
+  Groups g;
+  int N, K;
+  int tile16;      // fp8: the weights are in MOE_LAYOUT_TILE16
+  int accumulate;  // wgrad: add to out
+  int p_tiles, q_tiles, chunk;  // set by the launcher
+};
+
+// rows: about how many rows all groups hold together; it picks the kernel, never the result's meaning.
+hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s);
+hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStream_t s);
+hipError_t launch_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale, hipStream_t s);
+
 }  // namespace qmoe

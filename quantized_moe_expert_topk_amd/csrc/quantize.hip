@@ -1,0 +1,76 @@
+// quantize.hip -- bf16 rows to e4m3 codes with one fp32 scale per row and block of 128.
+//
+//   scale[b, r] = max |x[r, k]| over the block / 448,   q[r, k] = e4m3(x[r, k] / scale[b, r])
+//
+// A workgroup owns 32 rows x 4 blocks; 16 lanes hold a block, 8 values each.
+#include "grouped_dev.h"
+
+namespace qmoe {
+namespace {
+
+constexpr int QROWS = 32, QBLOCKS = 4;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// Maximum of a 31-bit pattern over the 16 lanes of a row.
+__device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
+  v = max(v, dpp_u32<0xB1>(v));
+  v = max(v, dpp_u32<0x4E>(v));
+  v = max(v, dpp_u32<0x141>(v));
+  return max(v, dpp_u32<0x140>(v));
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale) {
+  __shared__ float sc[QBLOCKS][QROWS];
+  const int tid = threadIdx.x, blk = (tid >> 4) & 3, r4 = tid >> 6;  // a wave: one row, 4 blocks
+  const size_t row0 = (size_t)blockIdx.x * QROWS;
+  const int kb0 = blockIdx.y * QBLOCKS, k = kb0 * 128 + (tid & 63) * 8;
+  constexpr int NP = QROWS / 4;
+  frag8 v[NP];
+#pragma unroll
+  for (int i = 0; i < NP; i++) {
+    const size_t r = row0 + i * 4 + r4;
+    v[i].q = make_uint4(0, 0, 0, 0);
+    if (r < (size_t)M && k < K) v[i].q = *reinterpret_cast<const uint4 *>(x + r * K + k);
+  }
+#pragma unroll
+  for (int i = 0; i < NP; i++) {
+    const size_t r = row0 + i * 4 + r4;
+    // magnitudes as integers: a NaN in the block is its maximum and makes the whole block NaN
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) m = max(m, max((v[i].u[j] & 0x7FFFu) << 16, v[i].u[j] & 0x7FFF0000u));
+    const float s = __uint_as_float(row16_umax(m)) / 448.f;
+    const float d = s == 0.f ? 1.f : s;  // a block of zeros: scale 0, codes 0
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      f[2 * j] = __uint_as_float(v[i].u[j] << 16) / d;
+      f[2 * j + 1] = __uint_as_float(v[i].u[j] & 0xFFFF0000u) / d;
+    }
+    uint2 c;
+    c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], (int)c.x, true);
+    c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
+    c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], (int)c.y, true);
+    if (r < (size_t)M && k < K) *reinterpret_cast<uint2 *>(q + r * K + k) = c;
+    if ((tid & 15) == 0) sc[blk][i * 4 + r4] = s;
+  }
+  __syncthreads();
+  const int kb = kb0 + (tid >> 5);
+  const size_t r = row0 + (tid & 31);
+  if (tid < QBLOCKS * QROWS && kb * 128 < K && r < (size_t)M) scale[(size_t)kb * M + r] = sc[tid >> 5][tid & 31];
+}
+
+hipError_t launch_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale, hipStream_t s) {
+  const dim3 grid((M + QROWS - 1) / QROWS, ((K + 127) / 128 + QBLOCKS - 1) / QBLOCKS);
+  k_quantize_blocks<<<grid, 256, 0, s>>>(x, M, K, q, scale);
+  return hipGetLastError();
+}
+
+}  // namespace qmoe
