@@ -373,7 +373,7 @@ int moe_layer_forward(const void *x_bf16, int T, const void *w_router_bf16, cons
  * Sums are fp32 in a fixed order: results do not vary from call to call.  Values in rows of no
  * expert never reach another row; a NaN or infinity in a row of an expert reaches that row's
  * outputs (forward, dgrad) or that expert's gradient (wgrad) only.
- * Requires 1 <= E <= 1024, N and K multiples of 8 and at most 4 million, and 16-byte aligned
+ * Requires 1 <= E <= 1024, N and K multiples of 8 and at most 2 million, and 16-byte aligned
  * matrices; an output must not overlap an operand. */
 
 /* y[r, n] = sum_k x[r, k] w[e, n, k] for every row r of expert e.

@@ -12,9 +12,9 @@ using namespace qmoe;
 
 namespace {
 
-// A workgroup addresses at most 256 rows (or 64 rows of a strided operand) of one matrix with 31-bit
-// byte offsets from its own 64-bit base.
-constexpr long long kMaxPitch = (1LL << 31) / 256 - 16;
+// A workgroup addresses at most 256 rows of one matrix, of at most 4 bytes an element, with 31-bit byte
+// offsets from its own 64-bit base.
+constexpr int kMaxWidth = (int)((1LL << 31) / (256 * 4)) - 16;
 
 bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
@@ -69,7 +69,7 @@ int grouped(const char *fn, int prod, const void *a, const void *b, const int32_
   if (N < 1 || K < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: N=%d K=%d must be positive", fn, N, K);
   if (N % 8 || K % 8)
     return abi_fail(MOE_ERR_UNSUPPORTED, "%s: N=%d and K=%d must be multiples of 8 (16-byte loads)", fn, N, K);
-  if (2LL * N > kMaxPitch || 2LL * K > kMaxPitch)
+  if (N > kMaxWidth || K > kMaxWidth)
     return abi_fail(MOE_ERR_UNSUPPORTED, "%s: N=%d or K=%d too large", fn, N, K);
   if (int rc = check_out(fn, out_dtype)) return rc;
   if (accumulate && out_dtype != MOE_OUT_F32)
@@ -101,7 +101,8 @@ int block(const char *fn, const void *xq, const float *xs, const void *wq, const
           int out_dtype, void *stream) {
   if (N < 1 || K < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: N=%d K=%d must be positive", fn, N, K);
   if (K % 16) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: K=%d must be a multiple of 16 (16-byte loads)", fn, K);
-  if (K > kMaxPitch) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: K=%d too large", fn, K);
+  if (N > kMaxWidth || K > kMaxWidth)
+    return abi_fail(MOE_ERR_UNSUPPORTED, "%s: N=%d or K=%d too large", fn, N, K);
   if (layout != MOE_LAYOUT_ROWS && layout != MOE_LAYOUT_TILE16)
     return abi_fail(MOE_ERR_UNSUPPORTED, "%s: layout %d is neither MOE_LAYOUT_ROWS nor MOE_LAYOUT_TILE16", fn, layout);
   if (layout == MOE_LAYOUT_TILE16 && N % 16)

@@ -28,22 +28,16 @@ typedef short s16x4g __attribute__((ext_vector_type(4)));
 // A byte offset that every buffer resource made here refuses: the load returns zeros.
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// Buffer resource over [base, base + 2 GiB): rows, columns and stages outside the operand are kept
-// out by kNowhere, so the resource needs no size of its own and its base can follow the stages.
-__device__ __forceinline__ i32x4g wide_rsrc(const void *base) {
+// Buffer resource over [base, base + bytes), bytes < 2 GiB: loads past it return zeros.  Base and size are
+// the same in every lane; readfirstlane keeps them in scalar registers, where the loads need them.
+__device__ __forceinline__ i32x4g range_rsrc(const uint8_t *base, uint32_t bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   i32x4g r;
   r[0] = (int)__builtin_amdgcn_readfirstlane((uint32_t)b);
-  r[1] = (int)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
-  r[2] = 0x7FFFFFF0;
+  r[1] = (int)(__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) & 0xFFFFu);
+  r[2] = (int)__builtin_amdgcn_readfirstlane(bytes);
   r[3] = 0x00020000;
   return r;
-}
-
-__device__ __forceinline__ void rsrc_advance(i32x4g &r, uint32_t bytes) {
-  const uint64_t b = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + bytes;
-  r[0] = (int)(uint32_t)b;
-  r[1] = (int)(uint32_t)(b >> 32);
 }
 
 template <class T>
@@ -83,137 +77,158 @@ __device__ __forceinline__ void group_range(const Groups &g, int e, int &lo, int
   n = g.counts ? min(max(c, 0), g.M - lo) : min(max(c, lo), g.M) - lo;
 }
 
-// Row tile t of the groups cut into tiles of BM rows, expert after expert: its expert, first row and
-// rows (1..BM).  False past the last tile.  One wave's work: 64 experts at a time, an inclusive scan
-// of their tile counts.
-__device__ __forceinline__ bool find_row_tile(const Groups &g, int BM, int t, int &e, int &row0, int &rows) {
-  const int lane = lane_id();
-  int before = 0;
-  for (int e0 = 0; e0 < g.E; e0 += 64) {
-    int lo = 0, n = 0;
-    if (e0 + lane < g.E) group_range(g, e0 + lane, lo, n);
-    const int tiles = (n + BM - 1) / BM;
-    int incl = tiles;
+// The same for an expert that is the same in every lane, through scalar loads: a vector load would wait for
+// the wave's operand loads and stores in flight.
+__device__ __forceinline__ void group_range_uniform(const Groups &g, int e, int &lo, int &n) {
+  typedef const __attribute__((address_space(4))) int32_t *cp;
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int o = ((cp)(uintptr_t)g.offsets)[e];
+  const int c = g.counts ? ((cp)(uintptr_t)g.counts)[e] : ((cp)(uintptr_t)g.offsets)[e + 1];
+  lo = min(max(o, 0), g.M);
+  n = g.counts ? min(max(c, 0), g.M - lo) : min(max(c, lo), g.M) - lo;
+}
+
+// first[e] = row tiles (of BM rows) of the experts before e, first[E] = all of them, made by the whole
+// workgroup in LDS: the experts' tile counts, each thread's run of them summed, the sums scanned.
+constexpr int kMaxExperts = 1024;
+
+template <int THREADS>
+__device__ __forceinline__ void make_tile_table(const Groups &g, int BM, int32_t *first) {
+  constexpr int EPT = kMaxExperts / THREADS, W = THREADS / 64;
+  __shared__ int32_t totals[W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int tiles[EPT], sum = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
-    }
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    if (t < before + total) {
-      const uint64_t past = __ballot(before + incl > t);
-      const int src = __builtin_ctzll(past);
-      const int first = before + __builtin_amdgcn_readlane(incl - tiles, src);
-      const int l = __builtin_amdgcn_readlane(lo, src), c = __builtin_amdgcn_readlane(n, src);
-      e = e0 + src;
-      row0 = l + (t - first) * BM;
-      rows = min(BM, c - (t - first) * BM);
-      return true;
-    }
-    before += total;
+  for (int i = 0; i < EPT; i++) {
+    const int e = tid * EPT + i;
+    int lo = 0, n = 0;
+    if (e < g.E) group_range(g, e, lo, n);
+    tiles[i] = (n + BM - 1) / BM;
+    sum += tiles[i];
   }
-  return false;
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 63) totals[wave] = incl;
+  __syncthreads();
+  int at = incl - sum;
+#pragma unroll
+  for (int w = 0; w < W; w++) at += w < wave ? totals[w] : 0;
+#pragma unroll
+  for (int i = 0; i < EPT; i++) {
+    if (tid * EPT + i <= g.E) first[tid * EPT + i] = at;
+    at += tiles[i];
+  }
+  if (tid == THREADS - 1 && g.E == kMaxExperts) first[g.E] = at;
+  __syncthreads();
+}
+
+// The expert that row tile t < first[E] belongs to (one wave's work, the same in every lane).
+__device__ __forceinline__ int expert_of_tile(const int32_t *first, int E, int t) {
+  int e0 = 0;
+  for (;; e0 += 64) {
+    const uint64_t past = __ballot(first[min(e0 + lane_id() + 1, E)] > t);
+    if (past) return e0 + __builtin_ctzll(past);
+  }
 }
 
 // ------------------------------------------------------------------------------------- operand tiles
 
-// Row operand: LDS tile [R][128 bytes], 16-byte unit u of row r at unit u ^ ((r >> 1) & 7): 16
-// consecutive rows read at one unit touch each of the 64 banks once.
-template <int R, int THREADS>
+// Row operand: LDS tile [R][KB bytes], KB 64 or 128; the 16-byte unit u of row r lies at unit u ^ swz(r),
+// so that the 16 lanes which a ds_read_b128 serves together (16 consecutive rows at one unit, or 8 of them
+// at one unit and 8 at its neighbour) touch each of the 64 banks once.
+template <int KB>
+__device__ __forceinline__ int row_swz(int r) {
+  const int g = (r >> 2) & 3;
+  return KB == 128 ? (r >> 1) & 7 : ((2 * g) & 3) ^ (3 * (g >> 1));
+}
+
+// The resource of a stage spans the existing rows from the stage's first byte on (rows past them read
+// zeros); units past the row's end are cut off by the thread that loads them.
+template <int R, int THREADS, int KB>
 struct RowTile {
-  static constexpr int kBytes = R * 128, NL = R * 8 / THREADS;
-  static_assert(R * 8 % THREADS == 0 && THREADS % 128 == 0, "whole loads, one swizzle per thread");
-  uint32_t voff[NL];
+  static constexpr int kBytes = R * KB, UPR = KB / 16, NL = R * UPR / THREADS, RSTEP = THREADS / UPR;
+  static_assert(R * UPR % THREADS == 0 && RSTEP % 16 == 0, "whole loads, one swizzle per thread");
+  uint32_t voff, step;
   int unit;  // the unit of each row this thread loads
 
   // tile16: rows stored in 16-row tiles, 16-byte unit u of row r at (r / 16) * 16 * pitch + 256 u + 16 (r % 16)
-  __device__ __forceinline__ void init(int valid, uint32_t pitch, bool tile16) {
-    const int tid = threadIdx.x, r0 = tid / 8;
-    unit = (tid & 7) ^ ((r0 >> 1) & 7);
-#pragma unroll
-    for (int j = 0; j < NL; j++) {
-      const uint32_t r = r0 + j * (THREADS / 8);
-      const uint32_t at = tile16 ? (r & ~15u) * pitch + (r & 15u) * 16 + unit * 256 : r * pitch + unit * 16;
-      voff[j] = (int)r < valid ? at : kNowhere;
-    }
+  __device__ __forceinline__ void init(uint32_t pitch, bool tile16) {
+    const uint32_t tid = threadIdx.x, r = tid / UPR;
+    unit = (tid % UPR) ^ row_swz<KB>(r);
+    voff = tile16 ? (r & ~15u) * pitch + (r & 15u) * 16 + unit * 256 : r * pitch + unit * 16;
+    step = RSTEP * pitch;
   }
-  // left: 16-byte units of c that exist from this stage on
-  __device__ __forceinline__ void issue(const i32x4g &rs, uint32_t dst, int left) const {
-    const uint32_t d = dst + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-    if (left >= 8) {
-#pragma unroll
-      for (int j = 0; j < NL; j++) load_to_lds16(rs, voff[j], d + j * THREADS * 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NL; j++) load_to_lds16(rs, unit < left ? voff[j] : kNowhere, d + j * THREADS * 16);
-    }
+  __device__ __forceinline__ void load(const i32x4g &rs, uint32_t dst, int j, int left) const {
+    load_to_lds16(rs, unit < left ? voff + j * step : kNowhere, dst + j * THREADS * 16);
   }
 };
 
-// Column operand: LDS tile [64 c][C columns of 2 bytes], unit u (8 columns) of row c at u ^ swz(c):
-// the 4 rows x 64 bytes that 32 lanes of a transposed read touch fall on different banks.
-template <int C, int THREADS>
-struct ColTile {
-  static constexpr int kBytes = C * 128, UPR = C / 8, NL = 64 * UPR / THREADS, RSTEP = THREADS / UPR;
-  static_assert(C % 64 == 0 && 64 * UPR % THREADS == 0 && RSTEP % 4 == 0, "whole loads, one swizzle per thread");
-  uint32_t voff[NL];
-  int row;
+// Column operand: LDS tile [KB / 2 c][C columns of 2 bytes], unit u (8 columns) of row c at u ^ swz(c):
+// the 8 rows (c..c + 3, c + 8..c + 11) x 32 bytes that 32 lanes of a transposed read touch fall on
+// different banks.
+template <int C>
+__device__ __forceinline__ int col_swz(int c) {
+  return (C >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2) ^ ((c >> 3) & 1) << 1;
+}
 
-  static __device__ __forceinline__ int swz(int c) { return UPR >= 16 ? (c & 3) << 2 : ((c >> 1) & 1) << 2; }
+// The resource of a stage spans the existing rows c; columns past the matrix are cut off by their threads.
+template <int C, int THREADS, int KB>
+struct ColTile {
+  static constexpr int ROWS = KB / 2, kBytes = C * KB, UPR = C / 8, NL = ROWS * UPR / THREADS, RSTEP = THREADS / UPR;
+  static_assert(C % 64 == 0 && ROWS * UPR % THREADS == 0 && RSTEP % 16 == 0, "whole loads, one swizzle per thread");
+  uint32_t voff, step;
 
   __device__ __forceinline__ void init(int valid_units, uint32_t pitch) {
-    const int tid = threadIdx.x;
-    row = tid / UPR;
-    const int u = (tid % UPR) ^ swz(row);
-#pragma unroll
-    for (int j = 0; j < NL; j++) voff[j] = u < valid_units ? (uint32_t)(row + j * RSTEP) * pitch + u * 16 : kNowhere;
+    const int tid = threadIdx.x, r = tid / UPR, u = (tid % UPR) ^ col_swz<C>(r);
+    voff = u < valid_units ? (uint32_t)r * pitch + u * 16 : kNowhere;
+    step = RSTEP * pitch;
   }
-  // left: rows c that exist from this stage on
-  __device__ __forceinline__ void issue(const i32x4g &rs, uint32_t dst, int left) const {
-    const uint32_t d = dst + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-    if (left >= 64) {
-#pragma unroll
-      for (int j = 0; j < NL; j++) load_to_lds16(rs, voff[j], d + j * THREADS * 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NL; j++)
-        load_to_lds16(rs, row + j * RSTEP < left ? voff[j] : kNowhere, d + j * THREADS * 16);
-    }
+  __device__ __forceinline__ void load(const i32x4g &rs, uint32_t dst, int j, int) const {
+    // kNowhere + j * step stays past every resource: offsets are below 2 GiB
+    load_to_lds16(rs, voff + j * step, dst + j * THREADS * 16);
   }
 };
 
-// Fragments of v_mfma_f32_32x32x16_bf16: lane l holds index l % 32 of a 32-wide tile and
-// c = 16 ks + 8 (l / 32) + 0..7 of the stage.
+// Fragments of v_mfma_f32_16x16x32_bf16: lane l holds index l % 16 of a 16-wide tile and
+// c = 32 ks + 8 (l / 16) + 0..7 of the stage.  (The 16x16 form: at the card's power limit it ran at
+// 2.1 PFLOP/s on random operands held in registers, the 32x32x16 form at 1.8.)
+template <int KB>
 struct RowFrag {
-  uint32_t at[4];  // per ks
-  __device__ __forceinline__ void init(int first) {  // first: a multiple of 32
-    const int lane = lane_id(), r = first + (lane & 31), h = lane >> 5, s = (r >> 1) & 7;
+  uint32_t at[KB / 64];  // per ks
+  __device__ __forceinline__ void init(int first) {  // first: a multiple of 16
+    const int lane = lane_id(), r = first + (lane & 15), g = lane >> 4;
 #pragma unroll
-    for (int ks = 0; ks < 4; ks++) at[ks] = r * 128 + ((2 * ks + h) ^ s) * 16;
+    for (int ks = 0; ks < KB / 64; ks++) at[ks] = r * KB + ((4 * ks + g) ^ row_swz<KB>(r)) * 16;
   }
   __device__ __forceinline__ void read(const uint8_t *tile, int t, int ks, frag8 &f) const {
-    f.q = *reinterpret_cast<const uint4 *>(tile + at[ks] + t * 32 * 128);
+    f.q = *reinterpret_cast<const uint4 *>(tile + at[ks] + t * 16 * KB);
   }
 };
 
-// T 32-column tiles of a column tile of C columns, from column `first` (a multiple of 32).
+// T 16-column tiles of a column tile of C columns, from column `first` (a multiple of 16).
 template <int C, int T>
 struct ColFrag {
-  uint32_t at[T];
+  // Tiles whose swizzled places repeat (8 of 16 columns: 128 columns) share an address.
+  static constexpr int NT = T < 8 ? T : 8;
+  uint32_t at[NT];
   __device__ __forceinline__ void init(int first) {
     const int lane = lane_id(), g = lane >> 4, i = lane & 15;
-    // the row this lane addresses in read 0 at ks 0; read 1 and the other ks add multiples of 4, which
-    // leave the swizzle as it is
-    const int c = 8 * (g >> 1) + (i >> 2);
+    // the row this lane addresses in read 0 at ks 0; read 1 adds 4 and ks adds multiples of 32, which leave
+    // the swizzle as it is
+    const int c = 8 * g + (i >> 2);
 #pragma unroll
-    for (int t = 0; t < T; t++) {
-      const int u = first / 8 + t * 4 + 2 * (g & 1) + ((i & 3) >> 1);
-      at[t] = c * C * 2 + (u ^ (C >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2)) * 16 + (i & 1) * 8;
+    for (int t = 0; t < NT; t++) {
+      const int u = first / 8 + t * 2 + ((i & 3) >> 1);
+      at[t] = c * C * 2 + (u ^ col_swz<C>(c)) * 16 + (i & 1) * 8;
     }
   }
   __device__ __forceinline__ void read(const uint8_t *tile, int t, int ks, frag8 &f) const {
     typedef __attribute__((address_space(3))) s16x4g *lp;
-    const uint8_t *p = tile + at[t] + ks * 16 * C * 2;
+    const uint8_t *p = tile + at[t % NT] + t / NT * NT * 32 + ks * 32 * C * 2;
     const s16x4g a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)p);
     const s16x4g b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 4 * C * 2));
     const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);

@@ -1,25 +1,56 @@
-// grouped_mm.hip -- bf16 products grouped by expert over ragged row ranges, and their gradients.
+// grouped_mm.hip -- bf16 products grouped by expert over ragged row ranges, and their gradients, gfx950.
+// product_dev.h holds the kernel; this file picks its tile.
 #include "product_dev.h"
 
 
 namespace qmoe {
 
+// 16-row tiles that `rows` rows of E experts make, about.
+long long few_row_tiles(const ProductArgs &a, int rows) {
+  return a.g.offsets ? rows / 16 + std::min(a.g.E, rows) : (rows + 15) / 16;
+}
+
+// Whether k_few_rows is the faster kernel: it costs about 4 us and moves 4.6 bytes of weights a ns, once per
+// 16 rows, while the tiled kernel with 128 x 32 outputs takes ring_us per 128-byte stage of the contraction
+// however few tiles there are (up to two a CU).  Measured (us, few / tiled): e4m3 16 x 4096 x 4096 6.8 / 19.8,
+// 64 x 4096 x 4096 18.0 / 20.2, 128 x 4096 x 4096 33.7 / 20.7; bf16, N 1024, K 2048: 8 experts of one row
+// 8.4 / 13.6, 8 of 16 rows 11.0 / 13.2, 32 of one row 25.4 / 22.0, 8 of 64 rows 33.2 / 13.5.
+bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
+  const double bytes = (double)a.K * elem;
+  const double few = 4 + few_row_tiles(a, rows) * bytes * a.N / 4.6e6;
+  const long long q = a.g.offsets ? rows / 32 + std::min(a.g.E, rows) : (rows + 31) / 32;
+  const double tiles = (double)q * ((a.N + 127) / 128);
+  return few < 2 + ring_us * (bytes + 127) / 128 * std::max(1.0, tiles / 512);
+}
+
+// Tiles by the mean rows of an expert, m (MI355X, 256 experts, N 1024, K 2048, us):
+//   forward   256 x 256   256 x 128   128 x 64   128 x 32       dgrad   256 x 256   256 x 128
+//   m = 256      361         357         471        767                    348         353
+//   m = 128      307         275         290        405                    300         254
+//   m = 64       282         248         224        251                    271         227
+//   m = 32       271         237         211        217                    259         210
+//   m = 8                                208        208
+// and 256 x 256 for large groups (8 experts of 2048 rows, N and K 4096: 428 against 484).
+// wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 517 against 659 for 256 x 128 and
+// 746 for 128 x 128), unless those are fewer tiles than CUs.
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
-  int v = mean > 192 ? 0 : mean > 48 ? 1 : mean > 32 ? 2 : 3;
+  int v = mean > 256 ? 0 : mean > 96 ? 4 : mean > 32 ? 2 : 3;
+  if (prod == kForward && few_rows_faster(a, rows, 2, 0.34)) v = 6;
+  if (prod == kWgrad) v = (long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256 ? 0 : 1;
   if (prod == kForward) {
-    if (v == 0) return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
-    if (v == 1) return run_product<kForward, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
-    if (v == 2) return run_product<kForward, kBf16, 128, 64, 2, 2, 3>(a, out_bf16, s);
-    return run_product<kForward, kBf16, 128, 32, 4, 1, 4>(a, out_bf16, s);
+    if (v == 6) return launch_few_rows(a, false, out_bf16, s);
+    if (v == 0) return run_product<kForward, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+    if (v == 4) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
+    if (v == 2) return run_product<kForward, kBf16, 128, 64, 2, 2, 128, 3>(a, out_bf16, s);
+    return run_product<kForward, kBf16, 128, 32, 4, 1, 128, 3>(a, out_bf16, s);
   }
   if (prod == kDgrad) {
-    if (v == 0) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
-    if (v == 1) return run_product<kDgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
-    return run_product<kDgrad, kBf16, 128, 32, 4, 1, 4>(a, out_bf16, s);
+    if (v == 0) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+    return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
   }
-  if (v == 0) return run_product<kWgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
-  return run_product<kWgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
+  if (v == 0) return run_product<kWgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+  return run_product<kWgrad, kBf16, 128, 128, 2, 2, 128, 2>(a, out_bf16, s);
 }
 
 }  // namespace qmoe

@@ -5,20 +5,31 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "grouped_dev.h"
 
 namespace qmoe {
 
-// v_mfma_f32_32x32x64_f8f6f4 with both operands e4m3 and no block scales: lane l holds index l % 32
-// and 32 bytes of c for its half l / 32 (any 32, as long as both operands take the same).
-__device__ __forceinline__ f32x16_t mfma32_e4m3(const frag8 &a0, const frag8 &a1, const frag8 &b0, const frag8 &b1,
-                                                f32x16_t c) {
+// v_mfma_f32_16x16x128_f8f6f4 with both operands e4m3 and no block scales: lane l holds index l % 16 and
+// 32 bytes of c for its group l / 16 (any 32, as long as both operands take the same).
+__device__ __forceinline__ f32x4_t mfma_e4m3(const frag8 &a0, const frag8 &a1, const frag8 &b0, const frag8 &b1,
+                                             f32x4_t c) {
   const i32x8_t a = {(int)a0.u[0], (int)a0.u[1], (int)a0.u[2], (int)a0.u[3],
                      (int)a1.u[0], (int)a1.u[1], (int)a1.u[2], (int)a1.u[3]};
   const i32x8_t b = {(int)b0.u[0], (int)b0.u[1], (int)b0.u[2], (int)b0.u[3],
                      (int)b1.u[0], (int)b1.u[1], (int)b1.u[2], (int)b1.u[3]};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// f(0), ..., f(N - 1) with compile-time indices (register arrays need them; the unroller gives up on long loops).
+template <class F, int... I>
+__device__ __forceinline__ void static_for_seq(F &&f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  static_for_seq(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
 // Operand types.  kFp8Native multiplies e4m3 in the fp8 MFMA, whose sums are not fp32 throughout: as
@@ -28,257 +39,436 @@ __device__ __forceinline__ f32x16_t mfma32_e4m3(const frag8 &a0, const frag8 &a1
 // seen on random codes: 1.1e-4 of the sum of magnitudes; about 3e-5 of the result's norm), far below a
 // bf16 output's own rounding (2^-9) and far above an fp32 one's.  kFp8Exact multiplies the codes as
 // bf16, which holds every e4m3 value and whose MFMA adds in fp32, at half the rate.
+constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
 constexpr int kBf16 = 0, kFp8Native = 1, kFp8Exact = 2;
 
-template <int PROD, int BP, int BQ, int WP, int WQ>
+template <int PROD, int BP, int BQ, int WP, int WQ, int KB>
 struct ProductTypes {
-  static constexpr int THREADS = 64 * WP * WQ, TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  static constexpr int THREADS = 64 * WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
   static constexpr bool A_ROWS = PROD == kForward, B_ROWS = PROD != kWgrad;
-  using ATile = std::conditional_t<A_ROWS, RowTile<BP, THREADS>, ColTile<BP, THREADS>>;
-  using BTile = std::conditional_t<B_ROWS, RowTile<BQ, THREADS>, ColTile<BQ, THREADS>>;
-  using AFrag = std::conditional_t<A_ROWS, RowFrag, ColFrag<BP, TP>>;
-  using BFrag = std::conditional_t<B_ROWS, RowFrag, ColFrag<BQ, TQ>>;
+  using ATile = std::conditional_t<A_ROWS, RowTile<BP, THREADS, KB>, ColTile<BP, THREADS, KB>>;
+  using BTile = std::conditional_t<B_ROWS, RowTile<BQ, THREADS, KB>, ColTile<BQ, THREADS, KB>>;
+  using AFrag = std::conditional_t<A_ROWS, RowFrag<KB>, ColFrag<BP, TP>>;
+  using BFrag = std::conditional_t<B_ROWS, RowFrag<KB>, ColFrag<BQ, TQ>>;
 };
 
-template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WP * WQ) void k_product(ProductArgs a) {
-  using T = ProductTypes<PROD, BP, BQ, WP, WQ>;
-  constexpr bool FP8 = DT != kBf16;
+// One output tile and the part of the contraction that it sums.
+struct OutTile {
+  int e, p0, q0, rows;  // rows: output rows q0, q0 + 1, ... that exist
+  int row0, len;        // wgrad: the expert's rows; len: the contraction's length in `per` units below
+};
+
+// Workgroups are persistent: each takes a sequence of tiles, and its loads run NS stages ahead of its products
+// across the tiles' borders, so that only the first tile waits for its first loads, and a tile's stores
+// leave while the next one's operands arrive.
+template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int KB, int NS, int OUT>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
+  using T = ProductTypes<PROD, BP, BQ, WP, WQ, KB>;
+  constexpr bool FP8 = DT != kBf16, OUT_BF16 = OUT == kOutBf16;
   constexpr int TP = T::TP, TQ = T::TQ;
   constexpr int XS_BYTES = FP8 ? 4 * (BQ > 64 ? BQ : 64) : 0;
   constexpr int STAGE = T::ATile::kBytes + T::BTile::kBytes + XS_BYTES;
+  constexpr bool WARM = BP == 256 && BQ == 256;  // warm(), below
   constexpr int LOADS = T::ATile::NL + T::BTile::NL + (FP8 ? 1 : 0);  // per thread and stage
+  constexpr int OPS = LOADS + (WARM ? 1 : 0);                         // with warm()
   constexpr int ES = FP8 ? 1 : 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  __shared__ int32_t first[PROD == kWgrad ? 1 : kMaxExperts + 1];
+  __shared__ __attribute__((aligned(256))) uint8_t unread[WARM ? 256 : 4];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave % WP, wq = wave / WP;
-
-  // Workgroup L runs on XCD L mod 8.  Runs of a.chunk consecutive tiles (which share operand rows) go to
-  // one XCD, the runs to the XCDs in turn.
-  const int b = blockIdx.x, span = 8 * a.chunk;
-  const int tile = b / span * span + (b % 8) * a.chunk + (b % span) / 8;
-  const int pt = tile % a.p_tiles, qt = tile / a.p_tiles;
-
-  const int p0 = pt * BP;
-  int e = 0, q0 = 0, rows = 0;     // q0: first output row of the tile; rows: output rows of the tile
-  int row0 = 0, n_rows = 0;        // wgrad: the expert's rows, the contraction
   const int P = PROD == kForward ? a.N : a.K;
-  if constexpr (PROD == kWgrad) {
-    e = qt / a.q_tiles;
-    if (e >= a.g.E) return;
-    q0 = (qt - e * a.q_tiles) * BQ;
-    rows = min(BQ, a.N - q0);
-    group_range(a.g, e, row0, n_rows);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
-    n_rows = __builtin_amdgcn_readfirstlane(n_rows);
-  } else if (a.g.offsets) {
-    if (!find_row_tile(a.g, BQ, qt, e, q0, rows)) return;
-  } else {
-    q0 = qt * BQ;
-    rows = min(BQ, a.g.M - q0);
-    if (rows <= 0) return;
-  }
 
-  typename T::ATile at;
-  typename T::BTile bt;
-  i32x4g ra, rb, rx;
-  uint32_t a_step, b_step;
-  int left, per;  // of the contraction, in what the tiles count: 16-byte units (rows) or rows (columns)
-  if constexpr (PROD == kForward) {
-    const uint32_t pitch = (uint32_t)a.K * ES;
-    ra = wide_rsrc(a.w + ((size_t)e * a.N + p0) * pitch);
-    at.init(a.N - p0, pitch, a.tile16);
-    a_step = a.tile16 ? 2048 : 128;
-    rb = wide_rsrc(a.x + (size_t)q0 * pitch);
-    bt.init(rows, pitch, false);
-    b_step = 128;
-    left = pitch / 16;
-    per = 8;
-  } else if constexpr (PROD == kDgrad) {
-    ra = wide_rsrc(a.w + ((size_t)e * a.N * a.K + p0) * 2);
-    at.init((a.K - p0) / 8, (uint32_t)a.K * 2);
-    a_step = 64 * (uint32_t)a.K * 2;
-    rb = wide_rsrc(a.x + (size_t)q0 * a.N * 2);
-    bt.init(rows, (uint32_t)a.N * 2, false);
-    b_step = 128;
-    left = a.N;  // in rows of w; the units of dy are a.N / 8
-    per = 64;
+  int q_total;  // q tiles
+  if constexpr (PROD == kWgrad) {
+    q_total = a.g.E * a.q_tiles;
+  } else if (a.g.offsets) {
+    make_tile_table<T::THREADS>(a.g, BQ, first);
+    q_total = __builtin_amdgcn_readfirstlane(first[a.g.E]);
   } else {
-    ra = wide_rsrc(a.w + ((size_t)row0 * a.K + p0) * 2);
-    at.init((a.K - p0) / 8, (uint32_t)a.K * 2);
-    a_step = 64 * (uint32_t)a.K * 2;
-    rb = wide_rsrc(a.x + ((size_t)row0 * a.N + q0) * 2);
-    bt.init((a.N - q0) / 8, (uint32_t)a.N * 2);
-    b_step = 64 * (uint32_t)a.N * 2;
-    left = n_rows;
-    per = 64;
+    q_total = (a.g.M + BQ - 1) / BQ;
   }
-  const int n_stages = (left + per - 1) / per;
-  const uint32_t lds0 = lds_addr(lds);
-  uint32_t xoff = 0;
-  if constexpr (FP8) {
-    rx = wide_rsrc(a.xs + q0);
-    const int r = (wave * 64) % (BQ > 64 ? BQ : 64) + lane;  // more waves than rows load the same scales again
-    xoff = r < rows ? r * 4 : kNowhere;
-  }
-  auto issue = [&](int slot) __attribute__((always_inline)) {
-    const uint32_t d = lds0 + slot * STAGE;
-    if constexpr (PROD == kDgrad) {
-      at.issue(ra, d, left);
-      bt.issue(rb, d + T::ATile::kBytes, left >> 3);
-    } else {
-      at.issue(ra, d, left);
-      bt.issue(rb, d + T::ATile::kBytes, left);
+  constexpr int PER = PROD == kForward ? KB / 16 : KB / 2;  // 16-byte units, or rows, of a stage
+
+  // Workgroup L runs on XCD L mod 8: of each round of gridDim.x tiles, an XCD takes a run of consecutive ones.
+  // The order is q_run (4, if there are as many) q tiles, then the next p: a run covers a block, which reads the fewest operand rows.
+  // Moves t on to the next tile that exists, from t itself; false past the last one.
+  auto locate = [&](int &t, OutTile &o) __attribute__((always_inline)) {
+    const int band = a.q_run * a.p_tiles;
+    for (;; t += gridDim.x) {
+      const int bq = t / band;
+      if (bq * a.q_run >= q_total) return false;
+      const int r = t - bq * band, pt = r / a.q_run, qt = bq * a.q_run + r % a.q_run;
+      if (qt >= q_total) continue;
+      o.p0 = pt * BP;
+      o.e = 0;
+      if constexpr (PROD == kWgrad) {
+        o.e = qt / a.q_tiles;
+        o.q0 = (qt - o.e * a.q_tiles) * BQ;
+        o.rows = min(BQ, a.N - o.q0);
+        group_range_uniform(a.g, o.e, o.row0, o.len);
+        o.row0 = __builtin_amdgcn_readfirstlane(o.row0);
+        o.len = __builtin_amdgcn_readfirstlane(o.len);
+      } else {
+        int lo = 0, n = a.g.M, f = 0;
+        if (a.g.offsets) {
+          o.e = __builtin_amdgcn_readfirstlane(expert_of_tile(first, a.g.E, qt));
+          f = __builtin_amdgcn_readfirstlane(first[o.e]);
+          group_range_uniform(a.g, o.e, lo, n);
+          lo = __builtin_amdgcn_readfirstlane(lo);
+          n = __builtin_amdgcn_readfirstlane(n);
+        }
+        o.q0 = lo + (qt - f) * BQ;
+        o.rows = min(BQ, n - (qt - f) * BQ);
+        o.len = PROD == kForward ? a.K * ES / 16 : a.N;
+      }
+      return true;
     }
-    if constexpr (FP8) {
-      load_to_lds4(rx, left > 0 ? xoff : kNowhere,
-                   d + T::ATile::kBytes + T::BTile::kBytes + (wave * 256) % XS_BYTES);
-      rsrc_advance(rx, (uint32_t)a.g.M * 4);
-    }
-    rsrc_advance(ra, a_step);
-    rsrc_advance(rb, b_step);
-    left -= per;
   };
 
+  // ---- the loads
+  // Base and size of a stage's operands: rows (matrix rows that exist) or columns (rows of the contraction
+  // left, at most a stage's).
+  typename T::ATile at;
+  typename T::BTile bt;
+  const uint8_t *pa = nullptr, *pb = nullptr;
+  const float *px = nullptr;
+  uint32_t size_a = 0, size_b = 0, size_x = 0;
+  int left = 0;  // of the contraction of the tile being loaded
+  int lt = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+  const uint32_t pitch_a = (uint32_t)a.K * ES, pitch_b = (uint32_t)(PROD == kForward ? a.K : a.N) * ES;
+  const uint32_t step_a = PROD != kForward ? KB / 2 * pitch_a : a.tile16 ? KB * 16 : KB;
+  const uint32_t step_b = PROD == kWgrad ? KB / 2 * pitch_b : KB;
+  uint32_t col_a = 0, col_b = 0;  // byte columns where a column operand starts
+  if constexpr (T::B_ROWS) bt.init(pitch_b, false);
+  if constexpr (T::A_ROWS) at.init(pitch_a, a.tile16);
+  const int xr = (wave * 64) % (BQ > 64 ? BQ : 64) + lane;  // more waves than rows load the same scales again
+  auto start = [&](const OutTile &o) __attribute__((always_inline)) {
+    left = o.len;
+    if constexpr (PROD == kForward) {
+      pa = a.w + ((size_t)o.e * a.N + o.p0) * pitch_a;
+      size_a = min(BP, a.N - o.p0) * pitch_a;
+    } else {
+      pa = a.w + (PROD == kDgrad ? (size_t)o.e * a.N : (size_t)o.row0) * pitch_a + o.p0 * 2;
+      col_a = o.p0 * 2;
+      at.init((a.K - o.p0) / 8, pitch_a);
+    }
+    if constexpr (PROD == kWgrad) {
+      pb = a.x + (size_t)o.row0 * pitch_b + o.q0 * 2;
+      col_b = o.q0 * 2;
+      bt.init((a.N - o.q0) / 8, pitch_b);
+    } else {
+      pb = a.x + (size_t)o.q0 * pitch_b;
+      size_b = o.rows * pitch_b;
+    }
+    if constexpr (FP8) {
+      px = a.xs + o.q0;
+      size_x = o.rows * 4;
+    }
+  };
+  // Load i of the LOADS that a thread issues per stage, into `slot`; open() before a stage's first one,
+  // close() after its last.  Past the last tile the loads fetch nothing.
+  const uint32_t lds0 = lds_addr(lds), lds_wave = lds0 + wave * 1024;
+  i32x4g ra, rb, rx;
+  auto open = [&]() __attribute__((always_inline)) {
+    if (left <= 0) {
+      OutTile o;
+      left = 0;
+      do {
+        lt += gridDim.x;
+        if (!locate(lt, o)) break;
+        if (o.len > 0) start(o);
+      } while (left == 0);
+    }
+    if constexpr (!T::A_ROWS) size_a = left > 0 ? min(left, KB / 2) * pitch_a - col_a : 0;
+    if constexpr (!T::B_ROWS) size_b = left > 0 ? min(left, KB / 2) * pitch_b - col_b : 0;
+    ra = range_rsrc(pa, left > 0 ? size_a : 0);
+    rb = range_rsrc(pb, left > 0 ? size_b : 0);
+    if constexpr (FP8) rx = range_rsrc(reinterpret_cast<const uint8_t *>(px), left > 0 ? size_x : 0);
+  };
+  auto load = [&](int slot, int i) __attribute__((always_inline)) {
+    const uint32_t d = lds_wave + slot * STAGE;
+    if (i < T::ATile::NL)
+      at.load(ra, d, i, left);
+    else if (i < T::ATile::NL + T::BTile::NL)
+      bt.load(rb, d + T::ATile::kBytes, i - T::ATile::NL, PROD == kDgrad ? left >> 3 : left);
+    else if constexpr (FP8)
+      load_to_lds4(rx, xr * 4, lds0 + slot * STAGE + T::ATile::kBytes + T::BTile::kBytes + (wave * 256) % XS_BYTES);
+  };
+  auto close = [&]() __attribute__((always_inline)) {
+    pa += step_a;
+    pb += step_b;
+    if constexpr (T::A_ROWS) size_a -= step_a;
+    if constexpr (T::B_ROWS) size_b -= step_b;
+    if constexpr (FP8) px += a.g.M;
+    left -= PER;
+  };
+  // Asks for lines of the stage after the next one, so that they are in this XCD's L2 when its loads go out:
+  // LDS has room for one stage of 256 x 256 ahead only, less than memory's latency.  The 4 q tiles that share an
+  // A panel, and 8 p tiles that share a B panel, each touch their part of it (4 bytes of every line).
+  const int wn = wave == 0 ? (lane * 4 + lt % 4) : (lane * 8 + lt / 4 % 8) & 255;  // line of the panel's 256
+  const bool wrow = wave == 0 ? T::A_ROWS : T::B_ROWS;
+  const uint32_t warm_pitch = wave == 0 ? pitch_a : pitch_b;
+  const uint32_t warm_off = !wrow                    ? wn / 4 * warm_pitch + wn % 4 * 128
+                            : wave == 0 && a.tile16 ? (wn & ~15) * warm_pitch + (wn & 15) * 128
+                                                    : wn * warm_pitch;
+  const uint32_t warm_dst = lds_addr(unread);
+  auto warm = [&]() __attribute__((always_inline)) {
+    if constexpr (WARM) {
+      // (called between close() and the next open(): pa, pb and left are the next stage's, the stage after it
+      // begins a step further and has left - PER of the contraction)
+      const bool more = left > PER && wave < 2;
+      const uint32_t step = wave == 0 ? step_a : step_b;
+      const uint32_t size = wrow ? (wave == 0 ? size_a : size_b) - step
+                                 : min(left - PER, KB / 2) * warm_pitch - (wave == 0 ? col_a : col_b);
+      const i32x4g r = range_rsrc((wave == 0 ? pa : pb) + step, more ? size : 0);
+      load_to_lds4(r, (wave == 1 && lane >= 32) ? kNowhere : warm_off, warm_dst);
+    }
+  };
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    open();
+#pragma unroll
+    for (int i = 0; i < LOADS; i++) load(slot, i);
+    close();
+    warm();
+  };
+
+  // ---- the products
+  OutTile o;
+  int ct = lt;
+  if (!locate(ct, o)) return;
+  lt = ct;
+  start(o);
   typename T::AFrag fa;
   typename T::BFrag fb;
-  fa.init(wp * TP * 32);
-  fb.init(wq * TQ * 32);
+  fa.init(wp * TP * 16);
+  fb.init(wq * TQ * 16);
+  f32x4_t acc[TP][TQ];
 
-  f32x16_t acc[TP][TQ];
-#pragma unroll
-  for (int p = 0; p < TP; p++)
-#pragma unroll
-    for (int q = 0; q < TQ; q++)
-#pragma unroll
-      for (int j = 0; j < 16; j++) acc[p][q][j] = 0.f;
+  // The stages that a tile's contraction takes.  bf16: the fragments of step ks + 1 are read while step ks
+  // multiplies, across the stages and tiles too: a stage's last step waits for the next stage's loads,
+  // meets the other waves, and reads ahead from it.  A wave issues in order, and all waves read after each
+  // barrier: reads and loads go one by one between the products, so that the matrix core has work while they
+  // queue.
+  constexpr int NKS = KB / 64, NM = TP * TQ, NR = TP + TQ;
+  frag8 af[2][TP], bf[2][TQ];
+  int slot = 0, odd = 0, stored = 0;
+  // Waits for all loads but the newest NS - 2 stages'.  Vector memory operations end in order: right after a tile's
+  // stores, those are newer than the loads awaited and may stay out.
+  constexpr int STORES = TP * TQ / (OUT_BF16 ? 2 : 1);
+  static_assert(!OUT_BF16 || TP % 2 == 0, "p tiles in pairs");
+  auto wait_loads = [&]() __attribute__((always_inline)) {
+    if (stored)
+      wait_vm<STORES + (NS - 2) * OPS + OPS - LOADS>();
+    else
+      wait_vm<(NS - 2) * OPS + OPS - LOADS>();
+    stored = 0;
+  };
+  auto read = [&](int sl, int ks, int to, int i) __attribute__((always_inline)) {  // b0 a0 b1 a1 ...
+    const uint8_t *ta = lds + sl * STAGE, *tb = ta + T::ATile::kBytes;
+    constexpr int BOTH = 2 * (TP < TQ ? TP : TQ);
+    const bool is_b = i < BOTH ? i % 2 == 0 : TQ > TP;
+    const int n = i < BOTH ? i / 2 : i - BOTH / 2;
+    if (is_b)
+      fb.read(tb, n, ks, bf[to][n]);
+    else
+      fa.read(ta, n, ks, af[to][n]);
+  };
+  auto multiply = [&](int from, int i) __attribute__((always_inline)) {
+    acc[i / TQ][i % TQ] = mfma_bf16(af[from][i / TQ], bf[from][i % TQ], acc[i / TQ][i % TQ]);
+  };
+  auto stage = [&](auto parity) __attribute__((always_inline)) {
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+    static_for<NKS>([&](auto ks) __attribute__((always_inline)) {
+      constexpr bool last = ks == NKS - 1;
+      constexpr int cur = (decltype(parity)::value + ks) & 1;
+      if constexpr (last) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_loads();
+        barrier_only();
+        open();
+      }
+      // the reads spread over the first RT of the step's ticks, the stage's loads over all of them
+      constexpr int TICKS = NM > NR ? NM : NR, RT = NM * 3 / 4 > NR ? NM * 3 / 4 : TICKS;
+      static_for<TICKS>([&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < NM) multiply(cur, i);
+        constexpr int r0 = (i * NR + RT - 1) / RT, r1 = ((i + 1) * NR + RT - 1) / RT;
+        static_for<(r1 < NR ? r1 : NR) - (r0 < NR ? r0 : NR)>([&](auto r) __attribute__((always_inline)) {
+          read(last ? next : slot, last ? 0 : ks + 1, cur ^ 1, r0 + r);
+        });
+        if constexpr (last) {
+          constexpr int j0 = i * LOADS / TICKS, j1 = (i + 1) * LOADS / TICKS;
+          static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(slot, j0 + j); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (last) {
+        close();
+        warm();
+      }
+    });
+    slot = next;
+  };
 
-  // fp8: the weight scales of the wave's 128-row block of w, 64 of them in the lanes
-  const float *ws = nullptr;
-  const int KB = (a.K + 127) / 128;
+  // fp8: a stage is one block of 128; its products go to a zero accumulator, scaled into the sum.
+  const int n_kb = (a.K + 127) / 128;
+  const float *ws = nullptr;  // the weight scales of the wave's 128-row block of w, 64 of them in the lanes
   float wsv = 0.f;
-  if constexpr (FP8) {
-    static_assert(TP * 32 <= 128, "one weight scale per wave and stage");
-    const int nb = min(p0 + wp * TP * 32, a.N - 1) / 128;
-    ws = a.ws + ((size_t)e * ((a.N + 127) / 128) + nb) * KB;
-  }
-
-#pragma unroll
-  for (int s = 0; s < NS - 1; s++) issue(s);
-  int slot = 0;
-  for (int s = 0; s < n_stages; s++) {
-    wait_vm<(NS - 2) * LOADS>();
+  auto stage_fp8 = [&](int s) __attribute__((always_inline)) {
+    static_assert(!FP8 || (KB == 128 && TP * 16 <= 128), "one weight scale per wave and stage");
+    wait_loads();
     barrier_only();
     issue(slot == 0 ? NS - 1 : slot - 1);
     const uint8_t *ta = lds + slot * STAGE, *tb = ta + T::ATile::kBytes;
     slot = slot == NS - 1 ? 0 : slot + 1;
-    if constexpr (FP8) {
-      if ((s & 63) == 0) wsv = ws[min(s + lane, KB - 1)];
-      const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), s & 63));
-      const float *tx = reinterpret_cast<const float *>(tb + T::BTile::kBytes);
-      float sx[TQ];
+    if ((s & 63) == 0) wsv = ws[min(s + lane, n_kb - 1)];
+    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), s & 63));
+    const float *tx = reinterpret_cast<const float *>(tb + T::BTile::kBytes);
+    float sx[TQ];
 #pragma unroll
-      for (int q = 0; q < TQ; q++) sx[q] = tx[wq * TQ * 32 + q * 32 + (lane & 31)] * sw;
-      constexpr int NB = DT == kFp8Native ? 4 : 8;  // MFMA operands per tile and stage: 16 e4m3 or 8 bf16 each
-      auto operand = [&](const auto &f, const uint8_t *t, int i, frag8 (&o)[NB]) __attribute__((always_inline)) {
+    for (int q = 0; q < TQ; q++) sx[q] = tx[wq * TQ * 16 + q * 16 + (lane & 15)] * sw;
+    constexpr int NB = DT == kFp8Native ? 2 : 4;  // MFMA operands per tile and stage: 16 e4m3 or 8 bf16 each
+    auto operand = [&](const auto &f, const uint8_t *t, int i, frag8 (&o)[NB]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          if constexpr (DT == kFp8Native) {
-            f.read(t, i, u, o[u]);
-          } else {
-            frag8 c;
-            f.read(t, i, u, c);
-            fp8x8_to_bf16(c.u[0], c.u[1], o[2 * u]);
-            fp8x8_to_bf16(c.u[2], c.u[3], o[2 * u + 1]);
-          }
-        }
-      };
-      frag8 bq[TQ][NB];
-#pragma unroll
-      for (int q = 0; q < TQ; q++) operand(fb, tb, q, bq[q]);
-#pragma unroll
-      for (int p = 0; p < TP; p++) {
-        frag8 ap[NB];
-        operand(fa, ta, p, ap);
-#pragma unroll
-        for (int q = 0; q < TQ; q++) {
-          f32x16_t t = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if constexpr (DT == kFp8Native) {
-            t = mfma32_e4m3(ap[0], ap[1], bq[q][0], bq[q][1], t);
-            t = mfma32_e4m3(ap[2], ap[3], bq[q][2], bq[q][3], t);
-          } else {
-#pragma unroll
-            for (int u = 0; u < NB; u++) t = mfma32_bf16(ap[u], bq[q][u], t);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; j++) acc[p][q][j] = fmaf(t[j], sx[q], acc[p][q][j]);
+      for (int u = 0; u < 2; u++) {
+        if constexpr (DT == kFp8Native) {
+          f.read(t, i, u, o[u]);
+        } else {
+          frag8 c;
+          f.read(t, i, u, c);
+          fp8x8_to_bf16(c.u[0], c.u[1], o[2 * u]);
+          fp8x8_to_bf16(c.u[2], c.u[3], o[2 * u + 1]);
         }
       }
-    } else {
+    };
+    frag8 bq[TQ][NB];
 #pragma unroll
-      for (int ks = 0; ks < 4; ks++) {
-        frag8 af[TP], bf[TQ];
+    for (int q = 0; q < TQ; q++) operand(fb, tb, q, bq[q]);
 #pragma unroll
-        for (int p = 0; p < TP; p++) fa.read(ta, p, ks, af[p]);
+    for (int p = 0; p < TP; p++) {
+      frag8 ap[NB];
+      operand(fa, ta, p, ap);
 #pragma unroll
-        for (int q = 0; q < TQ; q++) fb.read(tb, q, ks, bf[q]);
+      for (int q = 0; q < TQ; q++) {
+        f32x4_t t = zero4();
+        if constexpr (DT == kFp8Native) {
+          t = mfma_e4m3(ap[0], ap[1], bq[q][0], bq[q][1], t);
+        } else {
+#pragma unroll
+          for (int u = 0; u < NB; u++) t = mfma_bf16(ap[u], bq[q][u], t);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[p][q][j] = fmaf(t[j], sx[q], acc[p][q][j]);
+      }
+    }
+  };
+
+  // D register j of a lane: p = 4 (lane / 16) + j of the tile, q = lane % 16.  bf16: the lanes of two neighbouring
+  // p tiles trade halves, so that each holds 8 consecutive elements of one of them (16 bytes a store, and
+  // half the stores).  With P a multiple of 8 (bf16) or 4 a wave issues exactly STORES stores, whatever part
+  // of the tile exists (the resource refuses the rest).
+  auto store = [&]() __attribute__((always_inline)) {
+    constexpr uint32_t OS = OUT_BF16 ? 2 : 4;
+    const uint32_t pitch = (uint32_t)P * OS;
+    uint8_t *base = static_cast<uint8_t *>(a.out) + ((PROD == kWgrad ? (size_t)o.e * a.N : 0) + o.q0) * pitch;
+    const rsrc_t ro = make_rsrc(base, o.rows * pitch);
+    const int g = lane >> 4, c0 = o.p0 + wp * TP * 16;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (OUT == kOutAdd) {
+#pragma unroll
+      for (int q = 0; q < TQ; q++) {
+        const int r = wq * TQ * 16 + q * 16 + (lane & 15);
+#pragma unroll
+        for (int p = 0; p < TP; p++) {
+          const int c = c0 + p * 16 + 4 * g;
+          if (r < o.rows && c < P) acc[p][q] += *reinterpret_cast<const f32x4_t *>(base + (size_t)r * pitch + c * OS);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < TQ; q++) {
+      const uint32_t row = (wq * TQ * 16 + q * 16 + (lane & 15)) * pitch;
+      if (P % (OUT_BF16 ? 8 : 4) == 0) {
+        if constexpr (OUT_BF16) {
+#pragma unroll
+          for (int p = 0; p < TP; p += 2) {
+            uint32_t h[2][2];  // [tile p, p + 1][elements 0, 1 and 2, 3]
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+              for (int i = 0; i < 2; i++)
+                h[t][i] = __builtin_bit_cast(uint32_t, pack_bf16(acc[p + t][q][2 * i], acc[p + t][q][2 * i + 1]));
+            // lanes of groups 0..3: (tile, groups) p 0,1; p + 1 0,1; p 2,3; p + 1 2,3
+            const auto lo = __builtin_amdgcn_permlane16_swap(h[0][0], h[1][0], false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap(h[0][1], h[1][1], false, false);
+            const int c = c0 + (p + (g & 1)) * 16 + 8 * (g >> 1);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro,
+                                                   (int)(c < P ? row + c * OS : kNowhere), 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < TP; p++) {
+            const int c = c0 + p * 16 + 4 * g;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[p][q]), ro,
+                                                   (int)(c < P ? row + c * OS : kNowhere), 0, 0);
+          }
+        }
+      } else {
 #pragma unroll
         for (int p = 0; p < TP; p++)
 #pragma unroll
-          for (int q = 0; q < TQ; q++) acc[p][q] = mfma32_bf16(af[p], bf[q], acc[p][q]);
+          for (int i = 0; i < 4; i++) {
+            const int c = c0 + p * 16 + 4 * g + i;
+            const int off = (int)(c < P ? row + c * OS : kNowhere);
+            if constexpr (OUT_BF16)
+              __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(acc[p][q][i]), ro, off, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[p][q][i]), ro, off, 0, 0);
+          }
       }
     }
-  }
-  wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
+    stored = P % (OUT_BF16 ? 8 : 4) == 0;
+  };
 
-  // D register j of a lane: p = 8 (j / 4) + 4 (lane / 32) + j % 4 of the tile, q = lane % 32
-  const size_t ld = P;
+  constexpr int AHEAD = FP8 ? NS - 1 : NS;  // stages loaded before the first one multiplies
 #pragma unroll
-  for (int q = 0; q < TQ; q++) {
-    const int r = wq * TQ * 32 + q * 32 + (lane & 31);
-    if (r >= rows) continue;
-    const size_t at0 = ((PROD == kWgrad ? (size_t)e * a.N : 0) + q0 + r) * ld;
+  for (int s = 0; s < AHEAD; s++) issue(s);
+  if constexpr (!FP8) {
+    wait_vm<(NS - 1) * OPS + OPS - LOADS>();
+    barrier_only();
+#pragma unroll
+    for (int i = 0; i < NR; i++) read(0, 0, 0, i);
+  }
+  for (;;) {
 #pragma unroll
     for (int p = 0; p < TP; p++)
 #pragma unroll
-      for (int jj = 0; jj < 4; jj++) {
-        const int c = p0 + wp * TP * 32 + p * 32 + jj * 8 + 4 * (lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = acc[p][q][jj * 4 + i];
-        if constexpr (OUT_BF16) {
-          uint16_t *o = static_cast<uint16_t *>(a.out) + at0 + c;
-          if (P % 4 == 0) {
-            if (c >= P) continue;
-            const bf16x2_t l = pack_bf16(v[0], v[1]), h = pack_bf16(v[2], v[3]);
-            *reinterpret_cast<uint2 *>(o) = make_uint2(__builtin_bit_cast(uint32_t, l), __builtin_bit_cast(uint32_t, h));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (c + i < P) o[i] = bf16_bits(v[i]);
-          }
-        } else {
-          float *o = static_cast<float *>(a.out) + at0 + c;
-          if (P % 4 == 0) {
-            if (c >= P) continue;
-            float4 f = make_float4(v[0], v[1], v[2], v[3]);
-            if (PROD == kWgrad && a.accumulate) {
-              const float4 old = *reinterpret_cast<const float4 *>(o);
-              f = make_float4(f.x + old.x, f.y + old.y, f.z + old.z, f.w + old.w);
-            }
-            *reinterpret_cast<float4 *>(o) = f;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (c + i < P) o[i] = v[i];
-          }
-        }
+      for (int q = 0; q < TQ; q++) acc[p][q] = zero4();
+    const int n_stages = (o.len + PER - 1) / PER;
+    if constexpr (FP8) {
+      const int nb = min(o.p0 + wp * TP * 16, a.N - 1) / 128;
+      ws = a.ws + ((size_t)o.e * ((a.N + 127) / 128) + nb) * n_kb;
+      for (int s = 0; s < n_stages; s++) stage_fp8(s);
+    } else if constexpr (NKS % 2 == 0) {
+      for (int s = 0; s < n_stages; s++) stage(std::integral_constant<int, 0>{});
+    } else {
+      for (int s = 0; s < n_stages; s++) {
+        if (odd)
+          stage(std::integral_constant<int, 1>{});
+        else
+          stage(std::integral_constant<int, 0>{});
+        odd ^= 1;
       }
+    }
+    store();
+    ct += gridDim.x;
+    if (!locate(ct, o)) break;
   }
+  wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
 }
 
-template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS>
+template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int KB, int NS>
 hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   const int P = PROD == kForward ? a.N : a.K;
   a.p_tiles = (P + BP - 1) / BP;
@@ -289,17 +479,23 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   } else {  // the most row tiles that groups of M rows together can have
     q = a.g.offsets ? a.g.M / BQ + std::min(a.g.E, a.g.M) : (a.g.M + BQ - 1) / BQ;
   }
-  const long long tiles = q * a.p_tiles;
-  a.chunk = a.p_tiles >= 32 ? a.p_tiles : 32 / a.p_tiles * a.p_tiles;
-  while (a.chunk > 1 && tiles < 8LL * a.chunk) a.chunk = (a.chunk + 1) / 2;  // few tiles: use every XCD
-  const long long grid = (tiles + 8LL * a.chunk - 1) / (8LL * a.chunk) * (8LL * a.chunk);
-  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidConfiguration;
+  a.q_run = (int)std::max(1LL, std::min(4LL, q));
+  const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
+  if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
+  constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) : 0)) + kMaxExperts * 4 + 512;
+  constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 3 : 1);
+  const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
+  const auto launch = [&](auto out) {
+    k_product<PROD, DT, BP, BQ, WP, WQ, KB, NS, decltype(out)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
+  };
   if (out_bf16)
-    k_product<PROD, DT, BP, BQ, WP, WQ, NS, true><<<dim3((unsigned)grid), 64 * WP * WQ, 0, s>>>(a);
-  else if constexpr (DT != kFp8Native)
-    k_product<PROD, DT, BP, BQ, WP, WQ, NS, false><<<dim3((unsigned)grid), 64 * WP * WQ, 0, s>>>(a);
-  else
+    launch(std::integral_constant<int, kOutBf16>{});
+  else if constexpr (DT == kFp8Native)
     return hipErrorInvalidValue;
+  else if constexpr (PROD == kWgrad)
+    a.accumulate ? launch(std::integral_constant<int, kOutAdd>{}) : launch(std::integral_constant<int, kOutF32>{});
+  else
+    launch(std::integral_constant<int, kOutF32>{});
   return hipGetLastError();
 }
 

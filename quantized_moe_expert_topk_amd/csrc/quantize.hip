@@ -50,8 +50,23 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int 
     float f[8];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      f[2 * j] = __uint_as_float(v[i].u[j] << 16) / d;
-      f[2 * j + 1] = __uint_as_float(v[i].u[j] & 0xFFFF0000u) / d;
+      f[2 * j] = __uint_as_float(v[i].u[j] << 16);
+      f[2 * j + 1] = __uint_as_float(v[i].u[j] & 0xFFFF0000u);
+    }
+    // x / d rounded to nearest, three operations an element: with r the rounded 1 / d and t = x r within one
+    // unit of the quotient, x - t d is exact in one fma and t + r (x - t d) rounds to the quotient (Markstein).
+    // Exact means no underflow: a quotient that e4m3 does not round to 0 is at least 2^-10, so d >= 2^-60 is
+    // far enough.  Blocks of other magnitudes (and NaN) divide.
+    if (d >= 0x1p-60f && d <= 0x1p60f) {
+      const float r = 1.f / d;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float t = f[j] * r;
+        f[j] = fmaf(r, fmaf(-t, d, f[j]), t);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) f[j] /= d;
     }
     uint2 c;
     c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
