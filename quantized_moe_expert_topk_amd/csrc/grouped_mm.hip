@@ -2,6 +2,7 @@
 // product_dev.h holds the kernel; this file picks its tile.
 #include "product_dev.h"
 
+#include <cstdlib>
 
 namespace qmoe {
 
@@ -38,6 +39,7 @@ hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_
   int v = mean > 256 ? 0 : mean > 96 ? 4 : mean > 32 ? 2 : 3;
   if (prod == kForward && few_rows_faster(a, rows, 2, 0.34)) v = 6;
   if (prod == kWgrad) v = (long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256 ? 0 : 1;
+  if (const char *x = getenv("QMOE_V")) v = atoi(x);
   if (prod == kForward) {
     if (v == 6) return launch_few_rows(a, false, out_bf16, s);
     if (v == 0) return run_product<kForward, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);

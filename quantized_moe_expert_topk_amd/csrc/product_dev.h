@@ -66,8 +66,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   using T = ProductTypes<PROD, BP, BQ, WP, WQ, KB>;
   constexpr bool FP8 = DT != kBf16, OUT_BF16 = OUT == kOutBf16;
   constexpr int TP = T::TP, TQ = T::TQ;
-  constexpr int XS_BYTES = FP8 ? 4 * (BQ > 64 ? BQ : 64) : 0;
-  constexpr int STAGE = T::ATile::kBytes + T::BTile::kBytes + XS_BYTES;
+  constexpr int XS_BYTES = FP8 ? 4 * (BQ > 64 ? BQ : 64) : 0, SCALES = FP8 ? XS_BYTES + 256 : 0;
+  static_assert(!FP8 || 256 * WP * WQ > XS_BYTES, "waves left for the weight scales");
+  constexpr int STAGE = T::ATile::kBytes + T::BTile::kBytes + SCALES;
   constexpr bool WARM = BP == 256 && BQ == 256;  // warm(), below
   constexpr int LOADS = T::ATile::NL + T::BTile::NL + (FP8 ? 1 : 0);  // per thread and stage
   constexpr int OPS = LOADS + (WARM ? 1 : 0);                         // with warm()
@@ -133,8 +134,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   typename T::ATile at;
   typename T::BTile bt;
   const uint8_t *pa = nullptr, *pb = nullptr;
-  const float *px = nullptr;
-  uint32_t size_a = 0, size_b = 0, size_x = 0;
+  const float *ps = nullptr;  // fp8: the scales that this wave loads, of the tile's rows of x or blocks of rows of w
+  uint32_t size_a = 0, size_b = 0, size_s = 0;
   int left = 0;  // of the contraction of the tile being loaded
   int lt = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
   const uint32_t pitch_a = (uint32_t)a.K * ES, pitch_b = (uint32_t)(PROD == kForward ? a.K : a.N) * ES;
@@ -143,7 +144,10 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   uint32_t col_a = 0, col_b = 0;  // byte columns where a column operand starts
   if constexpr (T::B_ROWS) bt.init(pitch_b, false);
   if constexpr (T::A_ROWS) at.init(pitch_a, a.tile16);
-  const int xr = (wave * 64) % (BQ > 64 ? BQ : 64) + lane;  // more waves than rows load the same scales again
+  const int n_kb = (a.K + 127) / 128;
+  const bool x_scales = wave * 256 < XS_BYTES;
+  const uint32_t scale_off = x_scales ? (wave * 64 + lane) * 4 : lane * n_kb * 4;
+  const uint32_t scale_dst = x_scales ? wave * 256 : XS_BYTES;  // (the other waves all load the same weight scales)
   auto start = [&](const OutTile &o) __attribute__((always_inline)) {
     left = o.len;
     if constexpr (PROD == kForward) {
@@ -163,14 +167,15 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
       size_b = o.rows * pitch_b;
     }
     if constexpr (FP8) {
-      px = a.xs + o.q0;
-      size_x = o.rows * 4;
+      const int nb = (a.N + 127) / 128, b0 = o.p0 / 128;
+      ps = x_scales ? a.xs + o.q0 : a.ws + ((size_t)o.e * nb + b0) * n_kb;
+      size_s = x_scales ? o.rows * 4 : (min((BP + 127) / 128, nb - b0) - 1) * n_kb * 4 + 4;
     }
   };
   // Load i of the LOADS that a thread issues per stage, into `slot`; open() before a stage's first one,
   // close() after its last.  Past the last tile the loads fetch nothing.
   const uint32_t lds0 = lds_addr(lds), lds_wave = lds0 + wave * 1024;
-  i32x4g ra, rb, rx;
+  i32x4g ra, rb, rs;
   auto open = [&]() __attribute__((always_inline)) {
     if (left <= 0) {
       OutTile o;
@@ -185,7 +190,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
     if constexpr (!T::B_ROWS) size_b = left > 0 ? min(left, KB / 2) * pitch_b - col_b : 0;
     ra = range_rsrc(pa, left > 0 ? size_a : 0);
     rb = range_rsrc(pb, left > 0 ? size_b : 0);
-    if constexpr (FP8) rx = range_rsrc(reinterpret_cast<const uint8_t *>(px), left > 0 ? size_x : 0);
+    if constexpr (FP8) rs = range_rsrc(reinterpret_cast<const uint8_t *>(ps), left > 0 ? size_s : 0);
   };
   auto load = [&](int slot, int i) __attribute__((always_inline)) {
     const uint32_t d = lds_wave + slot * STAGE;
@@ -194,14 +199,14 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
     else if (i < T::ATile::NL + T::BTile::NL)
       bt.load(rb, d + T::ATile::kBytes, i - T::ATile::NL, PROD == kDgrad ? left >> 3 : left);
     else if constexpr (FP8)
-      load_to_lds4(rx, xr * 4, lds0 + slot * STAGE + T::ATile::kBytes + T::BTile::kBytes + (wave * 256) % XS_BYTES);
+      load_to_lds4(rs, scale_off, lds0 + slot * STAGE + T::ATile::kBytes + T::BTile::kBytes + scale_dst);
   };
   auto close = [&]() __attribute__((always_inline)) {
     pa += step_a;
     pb += step_b;
     if constexpr (T::A_ROWS) size_a -= step_a;
     if constexpr (T::B_ROWS) size_b -= step_b;
-    if constexpr (FP8) px += a.g.M;
+    if constexpr (FP8) ps += x_scales ? a.g.M : 1;
     left -= PER;
   };
   // Asks for lines of the stage after the next one, so that they are in this XCD's L2 when its loads go out:
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   // queue.
   constexpr int NKS = KB / 64, NM = TP * TQ, NR = TP + TQ;
   frag8 af[2][TP], bf[2][TQ];
-  int slot = 0, odd = 0, stored = 0;
+  int slot = 0, stored = 0;
   // Waits for all loads but the newest NS - 2 stages'.  Vector memory operations end in order: right after a tile's
   // stores, those are newer than the loads awaited and may stay out.
   constexpr int STORES = TP * TQ / (OUT_BF16 ? 2 : 1);
@@ -278,11 +283,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   auto multiply = [&](int from, int i) __attribute__((always_inline)) {
     acc[i / TQ][i % TQ] = mfma_bf16(af[from][i / TQ], bf[from][i % TQ], acc[i / TQ][i % TQ]);
   };
-  auto stage = [&](auto parity) __attribute__((always_inline)) {
+  static_assert(DT != kBf16 || NKS % 2 == 0, "the fragment sets alternate within a stage");
+  auto stage = [&]() __attribute__((always_inline)) {
     const int next = slot == NS - 1 ? 0 : slot + 1;
     static_for<NKS>([&](auto ks) __attribute__((always_inline)) {
       constexpr bool last = ks == NKS - 1;
-      constexpr int cur = (decltype(parity)::value + ks) & 1;
+      constexpr int cur = ks & 1;
       if constexpr (last) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_loads();
@@ -312,52 +318,99 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   };
 
   // fp8: a stage is one block of 128; its products go to a zero accumulator, scaled into the sum.
-  const int n_kb = (a.K + 127) / 128;
-  const float *ws = nullptr;  // the weight scales of the wave's 128-row block of w, 64 of them in the lanes
-  float wsv = 0.f;
-  auto stage_fp8 = [&](int s) __attribute__((always_inline)) {
-    static_assert(!FP8 || (KB == 128 && TP * 16 <= 128), "one weight scale per wave and stage");
+  constexpr int WB = TP * 16 / 128 > 0 ? TP * 16 / 128 : 1;
+  static_assert(!FP8 || (KB == 128 && WB == 1 && (TP * 16 == 128 || 128 % (TP * 16) == 0)), "one weight scale a wave");
+  auto read_scales = [&](int sl, float (&sx)[TQ]) __attribute__((always_inline)) {
+    const float *t = reinterpret_cast<const float *>(lds + sl * STAGE + T::ATile::kBytes + T::BTile::kBytes);
+    const float sw = t[XS_BYTES / 4 + wp * TP * 16 / 128];
+#pragma unroll
+    for (int q = 0; q < TQ; q++) sx[q] = t[wq * TQ * 16 + q * 16 + (lane & 15)] * sw;
+  };
+
+  // In the fp8 matrix cores: as stage(), with the B operand of a whole stage and one p tile of A at a time in
+  // registers.  Before the last two p tiles the slot has been read, so the barrier comes there, and the next
+  // stage's operands are read between their products, B as the last products release its registers.
+  frag8 a8[3][2], b8[TQ][2];
+  float s8[TQ];
+  auto stage_native = [&]() __attribute__((always_inline)) {
+    static_assert(DT != kFp8Native || TP >= 4, "p tiles before and after the barrier");
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+    const uint8_t *ta = lds + slot * STAGE, *na = lds + next * STAGE, *nb = na + T::ATile::kBytes;
+    constexpr auto buf = [](int p) { return p == TP - 1 ? 2 : p & 1; };
+    f32x4_t t[2];
+    static_for<TP>([&](auto p) __attribute__((always_inline)) {
+      if constexpr (p == TP - 2) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_loads();
+        barrier_only();
+        open();
+      }
+      static_for<TQ>([&](auto q) __attribute__((always_inline)) {
+        constexpr int i = p * TQ + q;
+        t[i & 1] = mfma_e4m3(a8[buf(p)][0], a8[buf(p)][1], b8[q][0], b8[q][1], zero4());
+        if constexpr (i > 0) {  // the product before, while this one runs
+          constexpr int lp = (i - 1) / TQ, lq = (i - 1) % TQ;
+#pragma unroll
+          for (int j = 0; j < 4; j++) acc[lp][lq][j] = fmaf(t[(i - 1) & 1][j], s8[lq], acc[lp][lq][j]);
+        }
+        if constexpr (p < TP - 2) {
+          // A of p + 1, and in p = TP - 3 also that of the last p
+          constexpr int R = p == TP - 3 ? 4 : 2, r0 = q * R / TQ, r1 = (q + 1) * R / TQ;
+          static_for<r1 - r0>([&](auto r) __attribute__((always_inline)) {
+            constexpr int k = r0 + r, pp = p + 1 + k / 2;
+            fa.read(ta, pp, k % 2, a8[buf(pp)][k % 2]);
+          });
+        } else {
+          constexpr int TICKS = 2 * TQ, k = (p - (TP - 2)) * TQ + q;
+          if constexpr (p == TP - 1) {
+            if constexpr (q < 2) fa.read(na, 0, q, a8[0][q]);  // (free since p = TP - 2 ended)
+            fb.read(nb, q, 0, b8[q][0]);
+            fb.read(nb, q, 1, b8[q][1]);
+          }
+          constexpr int j0 = k * LOADS / TICKS, j1 = (k + 1) * LOADS / TICKS;
+          static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(slot, j0 + j); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    constexpr int L = TP * TQ - 1;
+#pragma unroll
+    for (int j = 0; j < 4; j++) acc[TP - 1][TQ - 1][j] = fmaf(t[L & 1][j], s8[TQ - 1], acc[TP - 1][TQ - 1][j]);
+    read_scales(next, s8);
+    close();
+    warm();
+    slot = next;
+  };
+
+  auto stage_fp8 = [&]() __attribute__((always_inline)) {
     wait_loads();
     barrier_only();
     issue(slot == 0 ? NS - 1 : slot - 1);
     const uint8_t *ta = lds + slot * STAGE, *tb = ta + T::ATile::kBytes;
-    slot = slot == NS - 1 ? 0 : slot + 1;
-    if ((s & 63) == 0) wsv = ws[min(s + lane, n_kb - 1)];
-    const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv), s & 63));
-    const float *tx = reinterpret_cast<const float *>(tb + T::BTile::kBytes);
     float sx[TQ];
-#pragma unroll
-    for (int q = 0; q < TQ; q++) sx[q] = tx[wq * TQ * 16 + q * 16 + (lane & 15)] * sw;
-    constexpr int NB = DT == kFp8Native ? 2 : 4;  // MFMA operands per tile and stage: 16 e4m3 or 8 bf16 each
-    auto operand = [&](const auto &f, const uint8_t *t, int i, frag8 (&o)[NB]) __attribute__((always_inline)) {
+    read_scales(slot, sx);
+    slot = slot == NS - 1 ? 0 : slot + 1;
+    auto operand = [&](const auto &f, const uint8_t *t, int i, frag8 (&o)[4]) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        if constexpr (DT == kFp8Native) {
-          f.read(t, i, u, o[u]);
-        } else {
-          frag8 c;
-          f.read(t, i, u, c);
-          fp8x8_to_bf16(c.u[0], c.u[1], o[2 * u]);
-          fp8x8_to_bf16(c.u[2], c.u[3], o[2 * u + 1]);
-        }
+        frag8 c;
+        f.read(t, i, u, c);
+        fp8x8_to_bf16(c.u[0], c.u[1], o[2 * u]);
+        fp8x8_to_bf16(c.u[2], c.u[3], o[2 * u + 1]);
       }
     };
-    frag8 bq[TQ][NB];
+    frag8 bq[TQ][4];
 #pragma unroll
     for (int q = 0; q < TQ; q++) operand(fb, tb, q, bq[q]);
 #pragma unroll
     for (int p = 0; p < TP; p++) {
-      frag8 ap[NB];
+      frag8 ap[4];
       operand(fa, ta, p, ap);
 #pragma unroll
       for (int q = 0; q < TQ; q++) {
         f32x4_t t = zero4();
-        if constexpr (DT == kFp8Native) {
-          t = mfma_e4m3(ap[0], ap[1], bq[q][0], bq[q][1], t);
-        } else {
 #pragma unroll
-          for (int u = 0; u < NB; u++) t = mfma_bf16(ap[u], bq[q][u], t);
-        }
+        for (int u = 0; u < 4; u++) t = mfma_bf16(ap[u], bq[q][u], t);
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[p][q][j] = fmaf(t[j], sx[q], acc[p][q][j]);
       }
@@ -431,14 +484,22 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
     stored = P % (OUT_BF16 ? 8 : 4) == 0;
   };
 
-  constexpr int AHEAD = FP8 ? NS - 1 : NS;  // stages loaded before the first one multiplies
+  constexpr int AHEAD = DT == kFp8Exact ? NS - 1 : NS;  // stages loaded before the first one multiplies
 #pragma unroll
   for (int s = 0; s < AHEAD; s++) issue(s);
-  if constexpr (!FP8) {
+  if constexpr (DT != kFp8Exact) {
     wait_vm<(NS - 1) * OPS + OPS - LOADS>();
     barrier_only();
+    if constexpr (DT == kFp8Native) {
 #pragma unroll
-    for (int i = 0; i < NR; i++) read(0, 0, 0, i);
+      for (int i = 0; i < 2 * TQ; i++) fb.read(lds + T::ATile::kBytes, i / 2, i % 2, b8[i / 2][i % 2]);
+#pragma unroll
+      for (int i = 0; i < 2; i++) fa.read(lds, 0, i, a8[0][i]);
+      read_scales(0, s8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NR; i++) read(0, 0, 0, i);
+    }
   }
   for (;;) {
 #pragma unroll
@@ -446,20 +507,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
 #pragma unroll
       for (int q = 0; q < TQ; q++) acc[p][q] = zero4();
     const int n_stages = (o.len + PER - 1) / PER;
-    if constexpr (FP8) {
-      const int nb = min(o.p0 + wp * TP * 16, a.N - 1) / 128;
-      ws = a.ws + ((size_t)o.e * ((a.N + 127) / 128) + nb) * n_kb;
-      for (int s = 0; s < n_stages; s++) stage_fp8(s);
-    } else if constexpr (NKS % 2 == 0) {
-      for (int s = 0; s < n_stages; s++) stage(std::integral_constant<int, 0>{});
+    if constexpr (DT == kFp8Exact) {
+      for (int s = 0; s < n_stages; s++) stage_fp8();
+    } else if constexpr (DT == kFp8Native) {
+      for (int s = 0; s < n_stages; s++) stage_native();
     } else {
-      for (int s = 0; s < n_stages; s++) {
-        if (odd)
-          stage(std::integral_constant<int, 1>{});
-        else
-          stage(std::integral_constant<int, 0>{});
-        odd ^= 1;
-      }
+      for (int s = 0; s < n_stages; s++) stage();
     }
     store();
     ct += gridDim.x;
@@ -482,7 +535,7 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   a.q_run = (int)std::max(1LL, std::min(4LL, q));
   const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
   if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
-  constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) : 0)) + kMaxExperts * 4 + 512;
+  constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) + 256 : 0)) + kMaxExperts * 4 + 512;
   constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 3 : 1);
   const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
   const auto launch = [&](auto out) {
