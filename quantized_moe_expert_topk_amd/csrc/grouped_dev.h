@@ -51,6 +51,11 @@ __device__ __forceinline__ void load_to_lds16(const i32x4g &r, uint32_t voff, ui
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(voff), "s"(r)
                : "memory");
 }
+// The same with the non-temporal hint, for bytes that no other workgroup will ask for.
+__device__ __forceinline__ void load_to_lds16_nt(const i32x4g &r, uint32_t voff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(dst), "v"(voff), "s"(r)
+               : "memory");
+}
 __device__ __forceinline__ void load_to_lds4(const i32x4g &r, uint32_t voff, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(dst), "v"(voff), "s"(r)
                : "memory");
@@ -162,8 +167,13 @@ struct RowTile {
     voff = tile16 ? (r & ~15u) * pitch + (r & 15u) * 16 + unit * 256 : r * pitch + unit * 16;
     step = RSTEP * pitch;
   }
+  template <bool NT = false>
   __device__ __forceinline__ void load(const i32x4g &rs, uint32_t dst, int j, int left) const {
-    load_to_lds16(rs, unit < left ? voff + j * step : kNowhere, dst + j * THREADS * 16);
+    const uint32_t at = unit < left ? voff + j * step : kNowhere, to = dst + j * THREADS * 16;
+    if constexpr (NT)
+      load_to_lds16_nt(rs, at, to);
+    else
+      load_to_lds16(rs, at, to);
   }
 };
 
@@ -187,9 +197,14 @@ struct ColTile {
     voff = u < valid_units ? (uint32_t)r * pitch + u * 16 : kNowhere;
     step = RSTEP * pitch;
   }
+  template <bool NT = false>
   __device__ __forceinline__ void load(const i32x4g &rs, uint32_t dst, int j, int) const {
     // kNowhere + j * step stays past every resource: offsets are below 2 GiB
-    load_to_lds16(rs, voff + j * step, dst + j * THREADS * 16);
+    const uint32_t at = voff + j * step, to = dst + j * THREADS * 16;
+    if constexpr (NT)
+      load_to_lds16_nt(rs, at, to);
+    else
+      load_to_lds16(rs, at, to);
   }
 };
 

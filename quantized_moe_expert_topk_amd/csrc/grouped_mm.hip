@@ -2,8 +2,6 @@
 // product_dev.h holds the kernel; this file picks its tile.
 #include "product_dev.h"
 
-#include <cstdlib>
-
 namespace qmoe {
 
 // 16-row tiles that `rows` rows of E experts make, about.
@@ -24,34 +22,33 @@ bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
   return few < 2 + ring_us * (bytes + 127) / 128 * std::max(1.0, tiles / 512);
 }
 
-// Tiles by the mean rows of an expert, m (MI355X, 256 experts, N 1024, K 2048, us):
-//   forward   256 x 256   256 x 128   128 x 64   128 x 32       dgrad   256 x 256   256 x 128
-//   m = 256      361         357         471        767                    348         353
-//   m = 128      307         275         290        405                    300         254
-//   m = 64       282         248         224        251                    271         227
-//   m = 32       271         237         211        217                    259         210
-//   m = 8                                208        208
+// Tiles by the mean rows of an expert, m (MI355X, 256 experts, N 1024, K 2048, us; nt: weights non-temporal):
+//   forward   256 x 256   256 x 128   256 x 128 nt   128 x 64 nt   128 x 32 nt     dgrad   256 x 256   256 x 128   nt
+//   m = 256      347         334                                                              340         347
+//   m = 200                  313           308                                                            338     328
+//   m = 128      299         269           243                                                293         242     217
+//   m = 64                                               198                                              221     188
+//   m = 2                                                              184                                191     161
 // and 256 x 256 for large groups (8 experts of 2048 rows, N and K 4096: 428 against 484).
-// wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 517 against 659 for 256 x 128 and
-// 746 for 128 x 128), unless those are fewer tiles than CUs.
+// wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 236 against 262 for 256 x 128 and 293 for
+// 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs.
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
-  int v = mean > 256 ? 0 : mean > 96 ? 4 : mean > 32 ? 2 : 3;
-  if (prod == kForward && few_rows_faster(a, rows, 2, 0.34)) v = 6;
-  if (prod == kWgrad) v = (long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256 ? 0 : 1;
-  if (const char *x = getenv("QMOE_V")) v = atoi(x);
   if (prod == kForward) {
-    if (v == 6) return launch_few_rows(a, false, out_bf16, s);
-    if (v == 0) return run_product<kForward, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
-    if (v == 4) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
-    if (v == 2) return run_product<kForward, kBf16, 128, 64, 2, 2, 128, 3>(a, out_bf16, s);
-    return run_product<kForward, kBf16, 128, 32, 4, 1, 128, 3>(a, out_bf16, s);
+    if (few_rows_faster(a, rows, 2, 0.34)) return launch_few_rows(a, false, out_bf16, s);
+    if (mean > 256) return run_product<kForward, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+    if (mean > 128) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
+    if (mean > 64) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3, true>(a, out_bf16, s);
+    if (mean > 32) return run_product<kForward, kBf16, 128, 64, 2, 2, 128, 3, true>(a, out_bf16, s);
+    return run_product<kForward, kBf16, 128, 32, 4, 1, 128, 3, true>(a, out_bf16, s);
   }
   if (prod == kDgrad) {
-    if (v == 0) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
-    return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
+    if (mean > 256) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+    if (mean > 128) return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
+    return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3, true>(a, out_bf16, s);
   }
-  if (v == 0) return run_product<kWgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
+  if ((long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256)
+    return run_product<kWgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
   return run_product<kWgrad, kBf16, 128, 128, 2, 2, 128, 2>(a, out_bf16, s);
 }
 

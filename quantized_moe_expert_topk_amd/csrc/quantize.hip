@@ -10,6 +10,16 @@ namespace {
 
 constexpr int QROWS = 32, QBLOCKS = 4;
 
+// The rows are read once and the codes written once: non-temporal both ways.
+__device__ __forceinline__ uint4 nt_load16(const uint16_t *p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)));
+}
+__device__ __forceinline__ void nt_store8(uint8_t *p, uint2 v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(u32x2{v.x, v.y}, reinterpret_cast<u32x2 *>(p));
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
@@ -36,7 +46,7 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int 
   for (int i = 0; i < NP; i++) {
     const size_t r = row0 + i * 4 + r4;
     v[i].q = make_uint4(0, 0, 0, 0);
-    if (r < (size_t)M && k < K) v[i].q = *reinterpret_cast<const uint4 *>(x + r * K + k);
+    if (r < (size_t)M && k < K) v[i].q = nt_load16(x + r * K + k);
   }
 #pragma unroll
   for (int i = 0; i < NP; i++) {
@@ -73,7 +83,7 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int 
     c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], (int)c.x, true);
     c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
     c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], (int)c.y, true);
-    if (r < (size_t)M && k < K) *reinterpret_cast<uint2 *>(q + r * K + k) = c;
+    if (r < (size_t)M && k < K) nt_store8(q + r * K + k, c);
     if ((tid & 15) == 0) sc[blk][i * 4 + r4] = s;
   }
   __syncthreads();
