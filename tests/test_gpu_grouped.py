@@ -75,6 +75,11 @@ COUNTS = {
     "long": [700, 0, 513],
     "many": [((7 * i) % 5) for i in range(130)],
     "wide": [300, 257, 255, 256],
+    # enough experts for each tile that the launchers pick by the mean number of rows
+    "mean 12": [((5 * i) % 25) for i in range(130)],
+    "mean 24": [((7 * i) % 49) for i in range(130)],
+    "mean 48": [((11 * i) % 97) for i in range(130)],
+    "mean 80": [((13 * i) % 161) for i in range(130)],
 }
 SIZES = [(8, 8), (64, 64), (136, 72), (264, 200), (256, 512), (520, 1032)]  # (N, K)
 
@@ -84,6 +89,8 @@ SIZES = [(8, 8), (64, 64), (136, 72), (264, 200), (256, 512), (520, 1032)]  # (N
 def test_forward_and_gradients(counts, NK):
     """All three products on integer-valued inputs (exact in fp32) and on normal ones (bound)."""
     N, K = NK
+    if counts.startswith("mean") and N * K not in (264 * 200, 520 * 1032):
+        pytest.skip("many experts at two sizes are enough")
     off, cnt, M = ranges(COUNTS[counts])
     E = len(COUNTS[counts])
     g = gen(len(counts) * 1000 + N + K)
@@ -296,3 +303,316 @@ def test_quantize_blocks_not_finite():
     assert torch.isinf(s[1, 2]) and torch.isnan(q[2, 200].float()) and int((q[2, 128:].float() == 0).sum()) == 127
     v, rs = quantize_ref(x[[0, 3]])
     assert torch.equal(q[[0, 3]].float().double(), v)
+
+
+# --------------------------------------------------------------------------------------- how the calls are made
+
+
+def ragged(seed=0, N=264, K=392, counts=(70, 0, 1, 33, 200, 16)):
+    off, cnt, M = ranges(list(counts))
+    g = gen(seed)
+    return dict(off=off, cnt=cnt, M=M, E=len(counts), N=N, K=K, x=ints(g, M, K), w=ints(g, len(counts), N, K),
+                dy=ints(g, M, N))
+
+
+def every_product(c, y, dx, dw, stream=None):
+    qm.moe_grouped_mm(c["x"], c["w"], c["off"], c["cnt"], c["M"], out=y, stream=stream)
+    qm.moe_grouped_mm_dgrad(c["dy"], c["w"], c["off"], c["cnt"], c["M"], out=dx, stream=stream)
+    qm.moe_grouped_mm_wgrad(c["dy"], c["x"], c["off"], c["cnt"], c["M"], out=dw, stream=stream)
+
+
+def outputs(c):
+    f32 = dict(dtype=torch.float32, device=DEV)
+    return (torch.zeros(c["M"], c["N"], **f32), torch.zeros(c["M"], c["K"], **f32),
+            torch.zeros(c["E"], c["N"], c["K"], **f32))
+
+
+def check_every(c, y, dx, dw):
+    for e, r in enumerate(rows_of(c["off"], c["cnt"])):
+        X, W, D = c["x"][r].double(), c["w"][e].double(), c["dy"][r].double()
+        assert torch.equal(y[r].double(), X @ W.t()) and torch.equal(dx[r].double(), D @ W)
+        assert torch.equal(dw[e].double(), D.t() @ X)
+
+
+def test_gradients_against_differences():
+    """y is linear in x and in w: for integers L(x + d) - L(x) with L = sum(y * dy) is sum(dx * d) exactly."""
+    c = ragged(1)
+    y, dx, dw = outputs(c)
+    every_product(c, y, dx, dw)
+    g = gen(2)
+    d, dW = ints(g, c["M"], c["K"], most=1), ints(g, c["E"], c["N"], c["K"], most=1)
+    lin = (qm.moe_grouped_mm(c["x"] + d, c["w"], c["off"], out_dtype=torch.float32).double() - y.double())
+    assert float((lin * c["dy"].double()).sum()) == float((dx.double() * d.double()).sum())
+    lin = (qm.moe_grouped_mm(c["x"], c["w"] + dW, c["off"], out_dtype=torch.float32).double() - y.double())
+    assert float((lin * c["dy"].double()).sum()) == float((dw.double() * dW.double()).sum())
+
+
+@pytest.mark.parametrize("E,N,K", [(6, 264, 392), (130, 520, 1032)])
+def test_wgrad_accumulates(E, N, K):
+    c = ragged(3, N, K, [(17 * i) % 40 for i in range(E)])
+    base = ints(gen(4), E, N, K).float()
+    dw = base.clone()
+    for n in (1, 2):
+        qm.moe_grouped_mm_wgrad(c["dy"], c["x"], c["off"], out=dw, accumulate=True)
+    for e, r in enumerate(rows_of(c["off"], c["cnt"])):
+        assert torch.equal(dw[e].double(), base[e].double() + 2 * (c["dy"][r].double().t() @ c["x"][r].double()))
+
+
+def test_no_rows_at_all():
+    w = ints(gen(5), 3, 16, 24)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    x, dy = torch.empty(0, 24, dtype=torch.bfloat16, device=DEV), torch.empty(0, 16, dtype=torch.bfloat16, device=DEV)
+    assert qm.moe_grouped_mm(x, w, off).shape == (0, 16) and qm.moe_grouped_mm_dgrad(dy, w, off).shape == (0, 24)
+    dw = torch.full((3, 16, 24), 7.0, device=DEV)
+    qm.moe_grouped_mm_wgrad(dy, x, off, out=dw, accumulate=True)
+    assert bool((dw == 7).all())
+    qm.moe_grouped_mm_wgrad(dy, x, off, out=dw)
+    assert bool((dw == 0).all())
+    q, s = qm.moe_quantize_blocks(torch.empty(0, 32, dtype=torch.bfloat16, device=DEV))
+    assert q.shape == (0, 32) and s.shape == (1, 0)
+
+
+def test_not_finite_stays_in_its_row_and_expert():
+    c = ragged(6)
+    y, dx, dw = outputs(c)
+    bad = 70 + 1 + 5  # a row of expert 3
+    c["x"][bad, 9] = float("nan")
+    c["dy"][bad, 3] = float("inf")
+    every_product(c, y, dx, dw)
+    assert bool(torch.isnan(y[bad]).all())
+    keep = torch.ones(c["M"], dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    assert bool(torch.isfinite(y[keep]).all()) and bool(torch.isfinite(dx[keep]).all())
+    assert not bool(torch.isfinite(dx[bad]).all())
+    for e in range(c["E"]):
+        assert bool(torch.isfinite(dw[e]).all()) == (e != 3)
+
+
+def test_bad_ranges_stay_inside():
+    """Device values that name rows outside the matrices are cut to them: what is asked for inside is right, and
+    no byte around the outputs changes."""
+    N, K, M, E = 136, 72, 100, 6
+    g = gen(7)
+    x, w, dy = ints(g, M, K), ints(g, E, N, K), ints(g, M, N)
+    off = torch.tensor([-50, 20, 90, 5000, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=DEV)
+    cnt = torch.tensor([20, 30, 2 ** 31 - 1, 9, 5, -3], dtype=torch.int32, device=DEV)
+    inside = [slice(0, 20), slice(20, 50), slice(90, 100), slice(0, 0), slice(0, 0), slice(0, 0)]
+    ybuf, xbuf = torch.full((M + 600, N), 7.0, device=DEV), torch.full((M + 600, K), 7.0, device=DEV)
+    y, dx = ybuf[300:300 + M], xbuf[300:300 + M]
+    dw = torch.full((E, N, K), 7.0, device=DEV)
+    qm.moe_grouped_mm(x, w, off, cnt, 60, out=y)
+    qm.moe_grouped_mm_dgrad(dy, w, off, cnt, 60, out=dx)
+    qm.moe_grouped_mm_wgrad(dy, x, off, cnt, 60, out=dw)
+    xq, xs = fp8_rows(g, M, 80, "ints")
+    wq, ws = fp8_weights(g, E, N, 80, "ints")
+    fbuf = torch.full((M + 600, N), 7.0, device=DEV)
+    qm.moe_grouped_block_mm(xq, xs, wq, ws, off, cnt, 60, out=fbuf[300:300 + M])
+    torch.cuda.synchronize()
+    for buf in (ybuf, xbuf, fbuf):
+        assert bool((buf[:300] == 7).all()) and bool((buf[300 + M:] == 7).all()) and bool((buf[350:390] == 7).all())
+    for e, r in enumerate(inside):
+        X, W, D = x[r].double(), w[e].double(), dy[r].double()
+        assert torch.equal(y[r].double(), X @ W.t()) and torch.equal(dx[r].double(), D @ W)
+        assert torch.equal(dw[e].double(), D.t() @ X)
+        check_fp8("bad ranges", fbuf[300:300 + M][r], dequant_rows(xq[r], xs[:, r]), dequant_weights(wq[e], ws[e]), "ints")
+
+
+def test_matrices_past_4_gib():
+    """Weights, gradients and rows whose byte offsets need more than 32 bits."""
+    E, N, K = 260, 4104, 2056  # 4.4 GB of bf16 weights, 8.8 GB of fp32 gradient
+    cnt = [0] * E
+    cnt[0], cnt[E - 1] = 3, 5
+    off, counts, M = ranges(cnt)
+    g = gen(8)
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV)
+    w[0], w[E - 1] = ints(g, N, K), ints(g, N, K)
+    x, dy = ints(g, M, K), ints(g, M, N)
+    y = qm.moe_grouped_mm(x, w, off, out_dtype=torch.float32)
+    dx = qm.moe_grouped_mm_dgrad(dy, w, off, out_dtype=torch.float32)
+    dw = qm.moe_grouped_mm_wgrad(dy, x, off, out_dtype=torch.float32)
+    for e, r in ((0, slice(0, 3)), (E - 1, slice(3, 8))):
+        X, W, D = x[r].double(), w[e].double(), dy[r].double()
+        assert torch.equal(y[r].double(), X @ W.t()) and torch.equal(dx[r].double(), D @ W)
+        assert torch.equal(dw[e].double(), D.t() @ X)
+    assert not bool(dw[E // 2].any())
+    del w, dw
+    M, N, K = 1_100_000, 72, 2048  # 4.5 GB of rows
+    lo = torch.tensor([5, M - 300], dtype=torch.int32, device=DEV)
+    n = torch.tensor([2, 300], dtype=torch.int32, device=DEV)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[5:7], x[M - 300:] = ints(g, 2, K), ints(g, 300, K)
+    w = ints(g, 2, N, K)
+    y = torch.zeros(M, N, dtype=torch.float32, device=DEV)
+    qm.moe_grouped_mm(x, w, lo, n, 302, out=y)
+    assert torch.equal(y[5:7].double(), x[5:7].double() @ w[0].double().t())
+    assert torch.equal(y[M - 300:].double(), x[M - 300:].double() @ w[1].double().t())
+    assert not bool(y[7:M - 300].any())
+    xq = torch.zeros(M * 2, 2048, dtype=FP8, device=DEV)
+    xs = torch.ones(16, M * 2, device=DEV)
+    xq[-40:], xs[:, -40:] = fp8_rows(g, 40, 2048, "ints")
+    wq, ws = fp8_weights(g, 1, N, 2048, "ints")
+    lo, n = torch.tensor([2 * M - 40], dtype=torch.int32, device=DEV), torch.tensor([40], dtype=torch.int32, device=DEV)
+    y = torch.zeros(2 * M, N, dtype=torch.float32, device=DEV)
+    qm.moe_grouped_block_mm(xq, xs, wq, ws, lo, n, 40, out=y)
+    check_fp8("rows past 4 GiB", y[-40:], dequant_rows(xq[-40:], xs[:, -40:]), dequant_weights(wq[0], ws[0]), "ints")
+
+
+def test_streams_and_repeats():
+    """Calls on two streams at once, each result as alone; the same call twice gives the same bits."""
+    cases = [ragged(10 + i, 520, 1032, [(17 * j + i) % 90 for j in range(60)]) for i in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [outputs(c) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, o, s in zip(cases, outs, streams):
+            every_product(c, *o, stream=s)
+    with torch.cuda.stream(streams[0]):  # the current stream of the device
+        third = outputs(cases[0])
+        every_product(cases[0], *third)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        check_every(c, *o)
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], third))
+    g = gen(12)
+    x, w = bf16(g, 900, 1032), bf16(g, 9, 520, 1032)
+    off, _, _ = ranges([100] * 9)
+    a, b = qm.moe_grouped_mm(x, w, off), qm.moe_grouped_mm(x, w, off)
+    assert torch.equal(a, b)
+
+
+def test_captured_and_replayed():
+    """A graph of every call, replayed with new inputs and new row ranges, and eager calls between the replays."""
+    c = ragged(20)
+    y, dx, dw = outputs(c)
+    xb = bf16(gen(21), c["M"], 400)
+    wq, ws = fp8_weights(gen(22), c["E"], 144, 400)
+    q, s = qm.moe_quantize_blocks(xb)
+    z = torch.zeros(c["M"], 144, device=DEV)
+    zd = torch.zeros(c["M"], 144, dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        every_product(c, y, dx, dw)
+        qm.moe_quantize_blocks(xb, q, s)
+        qm.moe_grouped_block_mm(q, s, wq, ws, c["off"], c["cnt"], c["M"], out=z)
+        qm.moe_block_mm(q, s, wq[0], ws[0], out=zd)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(4):
+        counts = torch.tensor([[70, 0, 1, 33, 200, 16], [0, 0, 0, 320, 0, 0], [53] * 6, [1, 2, 3, 4, 5, 6]][n], dtype=torch.int32)
+        c["cnt"].copy_(counts)
+        c["off"][:6].copy_(torch.cumsum(counts, 0) - counts)
+        for t in ("x", "dy"):
+            c[t].copy_(ints(gen(30 + n), *c[t].shape))
+        xb.copy_(bf16(gen(40 + n), *xb.shape))
+        for t in (y, dx, dw, z):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, dx, dw, q.view(torch.uint8), s, z, zd)]
+        check_every(c, y, dx, dw)
+        for t in (y, dx, dw, z):
+            t.zero_()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (y, dx, dw, q.view(torch.uint8), s, z, zd))), n
+
+
+def test_expected_rows_changes_no_result():
+    c = ragged(50)
+    for hint in (0, 1, 100, 10 ** 9):
+        y = torch.zeros(c["M"], c["N"], device=DEV)
+        qm.moe_grouped_mm(c["x"], c["w"], c["off"], c["cnt"], hint, out=y)
+        for e, r in enumerate(rows_of(c["off"], c["cnt"])):
+            assert torch.equal(y[r].double(), c["x"][r].double() @ c["w"][e].double().t())
+
+
+# --------------------------------------------------------------------------------------- together
+
+
+def _layer(fmt, T=75):
+    from oracle import oracle as O
+    from synth import synth as S
+    from tests.gpu_util import bf16_dev, device_bank, to_dev
+    cfg = S.LayerConfig(90, "small layer", fmt, 256, 8, 2, 256, False, (T,), ((0, 256),))
+    inp = S.layer_inputs(cfg, T)
+    x = bf16_dev(inp.x)
+    _, ids, wts, al = qm.moe_route_align(x, bf16_dev(inp.router), None, cfg.k, 16)
+    pairs = torch.cat([torch.arange(T * cfg.k, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)])
+    slots = al.sorted_ids.long().clamp(max=T * cfg.k)
+    return O, cfg, inp, x, ids, wts, al, pairs[slots] // cfg.k, slots, device_bank, to_dev
+
+
+def _combine(y, slots, wts, T, k):
+    """Row sums of the pairs by their weights."""
+    out = torch.zeros(T * k + 1, y.shape[1], dtype=torch.float64, device=DEV)
+    out[slots] = y.double()
+    return (out[:T * k].view(T, k, -1) * wts.double()[:, :, None]).sum(1)
+
+
+def test_a_layer_of_bf16_products_and_its_backward():
+    """gather, gate_up, SwiGLU, down and combine from the alignment's own arrays, against moe_expert_forward; then
+    the layer's backward against torch's on the same formula in 64 bits."""
+    O, cfg, inp, x, ids, wts, al, tok, slots, device_bank, to_dev = _layer("bf16")
+    T, k, I, H = 75, cfg.k, cfg.I, cfg.H
+    wg = to_dev(inp.routed.gate_up).view(torch.bfloat16)
+    wd = to_dev(inp.routed.down).view(torch.bfloat16)
+    rows = x[tok].contiguous()
+    ranges_of = (al.offsets, al.counts, T * k)
+    gu = qm.moe_grouped_mm(rows, wg, *ranges_of, out=torch.zeros(al.capacity, 2 * I, device=DEV))
+    act = (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).to(torch.bfloat16)
+    y = qm.moe_grouped_mm(act, wd, *ranges_of, out=torch.zeros(al.capacity, H, device=DEV))
+    got = _combine(y, slots, wts, T, k)
+    want = qm.moe_expert_forward(device_bank(inp.routed), None, x, wts, al, 0, I)
+    # the same sums of the same bf16 products in another order; act may round to its other neighbour
+    assert float((got - want.double()).abs().max()) <= 1e-2 * float(want.abs().max())
+
+    # backward of sum(out * G) for the rows of the pairs (G and the weights as bf16 gradients of y)
+    G = torch.randn(T, H, device=DEV, generator=gen(1))
+    pair_w = torch.cat([wts.reshape(-1), torch.zeros(1, device=DEV)])[slots]
+    dy = (G[tok] * pair_w[:, None]).to(torch.bfloat16)
+    da = qm.moe_grouped_mm_dgrad(dy, wd, *ranges_of, out=torch.zeros(al.capacity, I, device=DEV))
+    dwd = qm.moe_grouped_mm_wgrad(dy, act, *ranges_of, out_dtype=torch.float32)
+    sig = torch.sigmoid(gu[:, :I])
+    dgu = torch.cat([da * gu[:, I:] * sig * (1 + gu[:, :I] * (1 - sig)), da * gu[:, :I] * sig], 1).to(torch.bfloat16)
+    dx = qm.moe_grouped_mm_dgrad(dgu, wg, *ranges_of, out=torch.zeros(al.capacity, H, device=DEV))
+    dwg = qm.moe_grouped_mm_wgrad(dgu, rows, *ranges_of, out_dtype=torch.float32)
+    for e, r in enumerate(rows_of(al.offsets, al.counts)):
+        X = rows[r].double().requires_grad_()
+        Wg, Wd = wg[e].double().requires_grad_(), wd[e].double().requires_grad_()
+        z = X @ Wg.t()
+        a = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+        (a @ Wd.t() * dy[r].double()).sum().backward()
+        # act and dgu were rounded to bf16 (half a step 2^-9 of values that then spread over the sums) and gu's
+        # sums are fp32: the norms agree to a few steps
+        for a_, b_ in ((dwd[e], Wd.grad), (dwg[e], Wg.grad), (dx[r], X.grad)):
+            assert float((a_.double() - b_).norm()) <= 2 ** -7 * float(b_.norm()) + 1e-30
+
+
+def test_a_layer_of_fp8_products_on_a_packed_bank():
+    """quantise, gate_up, SwiGLU, quantise, down on a TILE16 bank: each product against 64 bits on its own
+    operands, the whole against moe_expert_forward within what e4m3 activations can do."""
+    O, cfg, inp, x, ids, wts, al, tok, slots, device_bank, to_dev = _layer("fp8blk")
+    T, k, I, H = 75, cfg.k, cfg.I, cfg.H
+    bank = device_bank(inp.routed)
+    rows = x[tok].contiguous()
+    ranges_of = (al.offsets, al.counts, T * k)
+    xq, xs = qm.moe_quantize_blocks(rows)
+    gu = qm.moe_grouped_block_mm(xq, xs, bank.gate_up, bank.gate_up_scale, *ranges_of, layout=bank.layout,
+                                 out=torch.zeros(al.capacity, 2 * I, device=DEV))
+    act = (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).to(torch.bfloat16)
+    aq, as_ = qm.moe_quantize_blocks(act)
+    y = qm.moe_grouped_block_mm(aq, as_, bank.down, bank.down_scale, *ranges_of, layout=bank.layout,
+                                out=torch.zeros(al.capacity, H, device=DEV))
+    for e, r in enumerate(rows_of(al.offsets, al.counts)):
+        codes = to_dev(inp.routed.gate_up)[e].view(FP8), to_dev(inp.routed.down)[e].view(FP8)
+        check_fp8("gate_up", gu[r], dequant_rows(xq[r], xs[:, r]), dequant_weights(codes[0], to_dev(inp.routed.gate_up_scale)[e]), "")
+        check_fp8("down", y[r], dequant_rows(aq[r], as_[:, r]), dequant_weights(codes[1], to_dev(inp.routed.down_scale)[e]), "")
+    got = _combine(y, slots, wts, T, k)
+    want = qm.moe_expert_forward(bank, None, x, wts, al, 0, I).double()
+    # each activation is off by at most 2^-4 of itself, evenly over +- that: 2^-4 / sqrt(3) = 3.6% in the norm for
+    # each of the three rounded inputs (x in gate and in up, and the activation): under 3 * 3.6% + a margin
+    assert float((got - want).norm() / want.norm()) <= 0.125
