@@ -16,6 +16,15 @@ namespace {
 // offsets from its own 64-bit base.
 constexpr int kMaxWidth = (int)((1LL << 31) / (256 * 4)) - 16;
 
+// Rows that leave room for rounding up to tiles in 32 bits.
+constexpr int kMaxRows = 0x7FFFFC00;
+
+int check_rows(const char *fn, int M) {
+  if (M < 0) return abi_fail(MOE_ERR_INVALID_ARG, "%s: M=%d is negative", fn, M);
+  if (M > kMaxRows) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: M=%d too large", fn, M);
+  return MOE_OK;
+}
+
 bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 struct Range {
@@ -36,7 +45,8 @@ int check_out(const char *fn, int out_dtype) {
 
 int check_groups(const char *fn, const int32_t *offsets, int E, int M, int expected_rows) {
   if (!offsets) return abi_fail(MOE_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
-  if (E < 1 || M < 0) return abi_fail(MOE_ERR_INVALID_ARG, "%s: E=%d must be positive and M=%d not negative", fn, E, M);
+  if (E < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: E=%d must be positive", fn, E);
+  if (int rc = check_rows(fn, M)) return rc;
   if (E > 1024) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: E=%d > 1024", fn, E);
   if (expected_rows < 0) return abi_fail(MOE_ERR_INVALID_ARG, "%s: expected_rows=%d is negative", fn, expected_rows);
   return MOE_OK;
@@ -158,7 +168,8 @@ int moe_grouped_mm_wgrad(const void *dy_bf16, const void *x_bf16, const int32_t 
 
 int moe_quantize_blocks(const void *x_bf16, int M, int K, void *q, float *scale, void *stream) {
   const char *fn = "moe_quantize_blocks";
-  if (M < 0 || K < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: M=%d must not be negative and K=%d positive", fn, M, K);
+  if (int rc = check_rows(fn, M)) return rc;
+  if (K < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: K=%d must be positive", fn, K);
   if (K % 16) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: K=%d must be a multiple of 16 (16-byte loads)", fn, K);
   if (K > 65535 * 512) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: K=%d too large", fn, K);
   const size_t n = (size_t)M * K, sb = (size_t)M * (((size_t)K + 127) / 128) * 4;
@@ -173,7 +184,7 @@ int moe_quantize_blocks(const void *x_bf16, int M, int K, void *q, float *scale,
 
 int moe_block_mm(const void *xq, const float *xs, const void *wq, const float *ws, int layout, int M, int N, int K,
                  void *y, int out_dtype, void *stream) {
-  if (M < 0) return abi_fail(MOE_ERR_INVALID_ARG, "moe_block_mm: M=%d is negative", M);
+  if (int rc = check_rows("moe_block_mm", M)) return rc;
   return block("moe_block_mm", xq, xs, wq, ws, layout, nullptr, nullptr, 1, M, 0, N, K, y, out_dtype, stream);
 }
 
