@@ -67,8 +67,10 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// A barrier of the workgroup that leaves vector memory operations in flight, but no LDS read of this wave: the
+// operand loads that follow may overwrite what it read.
 __device__ __forceinline__ void barrier_only() {
-  asm volatile("" ::: "memory");
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }

@@ -157,29 +157,53 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   const bool x_scales = wave * 256 < XS_BYTES;
   const uint32_t scale_off = x_scales ? (wave * 64 + lane) * 4 : lane * n_kb * 4;
   const uint32_t scale_dst = x_scales ? wave * 256 : XS_BYTES;  // (the other waves all load the same weight scales)
+  // Where a tile's operands lie: the first stage's bytes, and how many there are (rows) or the byte columns
+  // where they start (columns).
+  struct Source {
+    const uint8_t *a, *b;
+    uint32_t size_a, size_b, col_a, col_b;
+  };
+  auto source = [&](const OutTile &o) __attribute__((always_inline)) {
+    Source r;
+    r.col_a = T::A_ROWS ? 0 : o.p0 * 2;
+    r.col_b = T::B_ROWS ? 0 : o.q0 * 2;
+    if constexpr (PROD == kForward)
+      r.a = a.w + ((size_t)o.e * a.N + o.p0) * pitch_a;
+    else
+      r.a = a.w + (PROD == kDgrad ? (size_t)o.e * a.N : (size_t)o.row0) * pitch_a + r.col_a;
+    r.size_a = min(BP, a.N - o.p0) * pitch_a;
+    r.b = a.x + (PROD == kWgrad ? (size_t)o.row0 : (size_t)o.q0) * pitch_b + r.col_b;
+    r.size_b = o.rows * pitch_b;
+    return r;
+  };
   auto start = [&](const OutTile &o) __attribute__((always_inline)) {
+    const Source r = source(o);
     left = o.len;
-    if constexpr (PROD == kForward) {
-      pa = a.w + ((size_t)o.e * a.N + o.p0) * pitch_a;
-      size_a = min(BP, a.N - o.p0) * pitch_a;
-    } else {
-      pa = a.w + (PROD == kDgrad ? (size_t)o.e * a.N : (size_t)o.row0) * pitch_a + o.p0 * 2;
-      col_a = o.p0 * 2;
-      at.init((a.K - o.p0) / 8, pitch_a);
-    }
-    if constexpr (PROD == kWgrad) {
-      pb = a.x + (size_t)o.row0 * pitch_b + o.q0 * 2;
-      col_b = o.q0 * 2;
-      bt.init((a.N - o.q0) / 8, pitch_b);
-    } else {
-      pb = a.x + (size_t)o.q0 * pitch_b;
-      size_b = o.rows * pitch_b;
-    }
+    pa = r.a;
+    pb = r.b;
+    size_a = r.size_a;
+    size_b = r.size_b;
+    col_a = r.col_a;
+    col_b = r.col_b;
+    if constexpr (!T::A_ROWS) at.init((a.K - o.p0) / 8, pitch_a);
+    if constexpr (!T::B_ROWS) bt.init((a.N - o.q0) / 8, pitch_b);
     if constexpr (FP8) {
       const int nb = (a.N + 127) / 128, b0 = o.p0 / 128;
       ps = x_scales ? a.xs + o.q0 : a.ws + ((size_t)o.e * nb + b0) * n_kb;
       size_s = x_scales ? o.rows * 4 : (min((BP + 127) / 128, nb - b0) - 1) * n_kb * 4 + 4;
     }
+  };
+  // The next tile that has a contraction, after tile t (WARM: located a tile ahead of its loads, for warm()).
+  OutTile on;
+  on.len = 0;
+  auto find_next = [&]() __attribute__((always_inline)) {
+    do {
+      lt += gridDim.x;
+      if (!locate(lt, on)) {
+        on.len = 0;
+        break;
+      }
+    } while (on.len <= 0);
   };
   // Load i of the LOADS that a thread issues per stage, into `slot`; open() before a stage's first one,
   // close() after its last.  Past the last tile the loads fetch nothing.
@@ -187,13 +211,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   i32x4g ra, rb, rs;
   auto open = [&]() __attribute__((always_inline)) {
     if (left <= 0) {
-      OutTile o;
       left = 0;
-      do {
-        lt += gridDim.x;
-        if (!locate(lt, o)) break;
-        if (o.len > 0) start(o);
-      } while (left == 0);
+      if constexpr (!WARM) find_next();
+      if (on.len > 0) start(on);
+      if constexpr (WARM) {
+        if (left > 0) find_next();
+      }
     }
     if constexpr (!T::A_ROWS) size_a = left > 0 ? min(left, KB / 2) * pitch_a - col_a : 0;
     if constexpr (!T::B_ROWS) size_b = left > 0 ? min(left, KB / 2) * pitch_b - col_b : 0;
@@ -221,7 +244,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   // Asks for lines of the stage after the next one, so that they are in this XCD's L2 when its loads go out:
   // LDS has room for one stage of 256 x 256 ahead only, less than memory's latency.  The 4 q tiles that share an
   // A panel, and 8 p tiles that share a B panel, each touch their part of it (4 bytes of every line).
-  const int wn = wave == 0 ? (lane * 4 + lt % 4) : (lane * 8 + lt / 4 % 8) & 255;  // line of the panel's 256
+  const int t0 = blockIdx.x / 8;  // (the place in the XCD's run)
+  const int wn = wave == 0 ? (lane * 4 + t0 % 4) : (lane * 8 + t0 / 4 % 8) & 255;  // line of the panel's 256
   const bool wrow = wave == 0 ? T::A_ROWS : T::B_ROWS;
   const uint32_t warm_pitch = wave == 0 ? pitch_a : pitch_b;
   const uint32_t warm_off = !wrow                    ? wn / 4 * warm_pitch + wn % 4 * 128
@@ -230,13 +254,22 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   const uint32_t warm_dst = lds_addr(unread);
   auto warm = [&]() __attribute__((always_inline)) {
     if constexpr (WARM) {
-      // (called between close() and the next open(): pa, pb and left are the next stage's, the stage after it
-      // begins a step further and has left - PER of the contraction)
-      const bool more = left > PER && wave < 2;
+      // (called between close() and the next open(): pa, pb and left are the next stage's.)  The stage after the
+      // next one is in this tile, or the first or second one of the next tile.
       const uint32_t step = wave == 0 ? step_a : step_b;
-      const uint32_t size = wrow ? (wave == 0 ? size_a : size_b) - step
-                                 : min(left - PER, KB / 2) * warm_pitch - (wave == 0 ? col_a : col_b);
-      const i32x4g r = range_rsrc((wave == 0 ? pa : pb) + step, more ? size : 0);
+      const uint8_t *base = (wave == 0 ? pa : pb) + step;
+      uint32_t size = (wave == 0 ? size_a : size_b) - step, col = wave == 0 ? col_a : col_b;
+      int rest = left - PER;
+      if (rest <= 0) {
+        const Source r = source(on);
+        const int n = left > 0 ? 0 : 1;
+        base = (wave == 0 ? r.a : r.b) + n * step;
+        size = (wave == 0 ? r.size_a : r.size_b) - n * step;
+        col = wave == 0 ? r.col_a : r.col_b;
+        rest = on.len - n * PER;
+      }
+      if (!wrow) size = min(rest, KB / 2) * warm_pitch - col;
+      const i32x4g r = range_rsrc(base, rest > 0 && wave < 2 ? size : 0);
       load_to_lds4(r, (wave == 1 && lane >= 32) ? kNowhere : warm_off, warm_dst);
     }
   };
@@ -254,6 +287,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   if (!locate(ct, o)) return;
   lt = ct;
   start(o);
+  if constexpr (WARM) find_next();
   typename T::AFrag fa;
   typename T::BFrag fb;
   fa.init(wp * TP * 16);
@@ -299,7 +333,6 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
       constexpr bool last = ks == NKS - 1;
       constexpr int cur = ks & 1;
       if constexpr (last) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_loads();
         barrier_only();
         open();
@@ -349,7 +382,6 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
     f32x4_t t[2];
     static_for<TP>([&](auto p) __attribute__((always_inline)) {
       if constexpr (p == TP - 2) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_loads();
         barrier_only();
         open();
