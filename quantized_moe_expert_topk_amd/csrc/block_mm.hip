@@ -20,13 +20,13 @@ hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStr
   // (k_few_rows addresses the activation scales with 31 bits)
   if ((long long)a.g.M * ((a.K + 127) / 128) < (1 << 29) && few_rows_faster(a, rows, 1, 0.58))
     return launch_few_rows(a, true, out_bf16, s);
-  if (mean <= 16) return run_product<kForward, kFp8Exact, 128, 32, 4, 1, 128, 3, true>(a, out_bf16, s);
+  if (mean <= 16) return run_product<kForward, kFp8Exact, 128, 32, 4, 1, 3, true>(a, out_bf16, s);
   if (mean <= (out_bf16 && wide >= 128 ? 32 : 64))
-    return run_product<kForward, kFp8Exact, 128, 64, 2, 2, 128, 3, true>(a, out_bf16, s);
-  if (!out_bf16) return run_product<kForward, kFp8Exact, 128, 128, 2, 2, 128, 2>(a, out_bf16, s);
-  if (wide < 128) return run_product<kForward, kFp8Native, 128, 128, 2, 2, 128, 2>(a, out_bf16, s);
-  if (mean <= 64) return run_product<kForward, kFp8Native, 256, 128, 4, 2, 128, 3, true>(a, out_bf16, s);
-  return run_product<kForward, kFp8Native, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
+    return run_product<kForward, kFp8Exact, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
+  if (!out_bf16) return run_product<kForward, kFp8Exact, 128, 128, 2, 2, 2>(a, out_bf16, s);
+  if (wide < 128) return run_product<kForward, kFp8Native, 128, 128, 2, 2, 2>(a, out_bf16, s);
+  if (mean <= 64) return run_product<kForward, kFp8Native, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
+  return run_product<kForward, kFp8Native, 256, 128, 4, 2, 3>(a, out_bf16, s);
 }
 
 }  // namespace qmoe

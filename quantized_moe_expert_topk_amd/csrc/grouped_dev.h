@@ -40,6 +40,8 @@ __device__ __forceinline__ i32x4g range_rsrc(const uint8_t *base, uint32_t bytes
   return r;
 }
 
+constexpr int KB = 128;  // bytes of c per row (or column) and stage
+
 template <class T>
 __device__ __forceinline__ uint32_t lds_addr(T *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)p;
@@ -96,11 +98,15 @@ __device__ __forceinline__ void group_range_uniform(const Groups &g, int e, int 
 }
 
 // first[e] = row tiles (of BM rows) of the experts before e, first[E] = all of them, made by the whole
-// workgroup in LDS: the experts' tile counts, each thread's run of them summed, the sums scanned.
-constexpr int kMaxExperts = 1024;
+// workgroup in LDS: the experts' tile counts, each thread's run of them summed, the sums scanned.  Returns the
+// tiles to compute: disjoint ranges have at most M / BM + min(E, M), and no more are taken of ranges that
+// overlap.  Sums stop at kManyTiles, past any such number, so that no device value makes them overflow.
+constexpr int kMaxExperts = 1024, kManyTiles = 1 << 29;
+
+__device__ __forceinline__ int add_tiles(int a, int b) { return min(a + b, kManyTiles); }
 
 template <int THREADS>
-__device__ __forceinline__ void make_tile_table(const Groups &g, int BM, int32_t *first) {
+__device__ __forceinline__ int make_tile_table(const Groups &g, int BM, int32_t *first) {
   constexpr int EPT = kMaxExperts / THREADS, W = THREADS / 64;
   __shared__ int32_t totals[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -111,51 +117,50 @@ __device__ __forceinline__ void make_tile_table(const Groups &g, int BM, int32_t
     int lo = 0, n = 0;
     if (e < g.E) group_range(g, e, lo, n);
     tiles[i] = (n + BM - 1) / BM;
-    sum += tiles[i];
+    sum = add_tiles(sum, tiles[i]);
   }
-  int incl = sum;
+  int before = sum;  // of the wave's lanes up to this one, then of those before it
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
+    const int v = __shfl_up(before, d);
+    if (lane >= d) before = add_tiles(before, v);
   }
-  if (lane == 63) totals[wave] = incl;
+  if (lane == 63) totals[wave] = before;
+  before = __shfl_up(before, 1);
+  if (lane == 0) before = 0;
   __syncthreads();
-  int at = incl - sum;
 #pragma unroll
-  for (int w = 0; w < W; w++) at += w < wave ? totals[w] : 0;
+  for (int w = 0; w < W; w++)
+    if (w < wave) before = add_tiles(before, totals[w]);
 #pragma unroll
   for (int i = 0; i < EPT; i++) {
-    if (tid * EPT + i <= g.E) first[tid * EPT + i] = at;
-    at += tiles[i];
+    if (tid * EPT + i <= g.E) first[tid * EPT + i] = before;
+    before = add_tiles(before, tiles[i]);
   }
-  if (tid == THREADS - 1 && g.E == kMaxExperts) first[g.E] = at;
+  if (tid == THREADS - 1 && g.E == kMaxExperts) first[g.E] = before;
   __syncthreads();
+  return __builtin_amdgcn_readfirstlane(min(first[g.E], g.M / BM + min(g.E, g.M)));
 }
 
 // The expert that row tile t < first[E] belongs to (one wave's work, the same in every lane).
 __device__ __forceinline__ int expert_of_tile(const int32_t *first, int E, int t) {
-  int e0 = 0;
-  for (;; e0 += 64) {
+  for (int e0 = 0; e0 < E; e0 += 64) {
     const uint64_t past = __ballot(first[min(e0 + lane_id() + 1, E)] > t);
     if (past) return e0 + __builtin_ctzll(past);
   }
+  return E - 1;
 }
 
 // ------------------------------------------------------------------------------------- operand tiles
 
-// Row operand: LDS tile [R][KB bytes], KB 64 or 128; the 16-byte unit u of row r lies at unit u ^ swz(r),
-// so that the 16 lanes which a ds_read_b128 serves together (16 consecutive rows at one unit, or 8 of them
-// at one unit and 8 at its neighbour) touch each of the 64 banks once.
-template <int KB>
-__device__ __forceinline__ int row_swz(int r) {
-  const int g = (r >> 2) & 3;
-  return KB == 128 ? (r >> 1) & 7 : ((2 * g) & 3) ^ (3 * (g >> 1));
-}
+// Row operand: LDS tile [R][128 bytes]; the 16-byte unit u of row r lies at unit u ^ swz(r), so that the 16 lanes
+// which a ds_read_b128 serves together (16 consecutive rows at one unit, or 8 of them at one unit and 8 at its
+// neighbour) touch each of the 64 banks once (no bank conflicts counted, SQ_LDS_BANK_CONFLICT).
+__device__ __forceinline__ int row_swz(int r) { return (r >> 1) & 7; }
 
 // The resource of a stage spans the existing rows from the stage's first byte on (rows past them read
 // zeros); units past the row's end are cut off by the thread that loads them.
-template <int R, int THREADS, int KB>
+template <int R, int THREADS>
 struct RowTile {
   static constexpr int kBytes = R * KB, UPR = KB / 16, NL = R * UPR / THREADS, RSTEP = THREADS / UPR;
   static_assert(R * UPR % THREADS == 0 && RSTEP % 16 == 0, "whole loads, one swizzle per thread");
@@ -165,7 +170,7 @@ struct RowTile {
   // tile16: rows stored in 16-row tiles, 16-byte unit u of row r at (r / 16) * 16 * pitch + 256 u + 16 (r % 16)
   __device__ __forceinline__ void init(uint32_t pitch, bool tile16) {
     const uint32_t tid = threadIdx.x, r = tid / UPR;
-    unit = (tid % UPR) ^ row_swz<KB>(r);
+    unit = (tid % UPR) ^ row_swz(r);
     voff = tile16 ? (r & ~15u) * pitch + (r & 15u) * 16 + unit * 256 : r * pitch + unit * 16;
     step = RSTEP * pitch;
   }
@@ -182,20 +187,17 @@ struct RowTile {
 // Column operand: LDS tile [KB / 2 c][C columns of 2 bytes], unit u (8 columns) of row c at u ^ swz(c):
 // the 8 rows (c..c + 3, c + 8..c + 11) x 32 bytes that 32 lanes of a transposed read touch fall on
 // different banks.
-template <int C>
-__device__ __forceinline__ int col_swz(int c) {
-  return (C >= 128 ? (c & 3) << 2 : ((c >> 1) & 1) << 2) ^ ((c >> 3) & 1) << 1;
-}
+__device__ __forceinline__ int col_swz(int c) { return (c & 3) << 2 ^ ((c >> 3) & 1) << 1; }
 
 // The resource of a stage spans the existing rows c; columns past the matrix are cut off by their threads.
-template <int C, int THREADS, int KB>
+template <int C, int THREADS>
 struct ColTile {
   static constexpr int ROWS = KB / 2, kBytes = C * KB, UPR = C / 8, NL = ROWS * UPR / THREADS, RSTEP = THREADS / UPR;
-  static_assert(C % 64 == 0 && ROWS * UPR % THREADS == 0 && RSTEP % 16 == 0, "whole loads, one swizzle per thread");
+  static_assert(C % 128 == 0 && ROWS * UPR % THREADS == 0 && RSTEP % 16 == 0, "whole loads, one swizzle per thread");
   uint32_t voff, step;
 
   __device__ __forceinline__ void init(int valid_units, uint32_t pitch) {
-    const int tid = threadIdx.x, r = tid / UPR, u = (tid % UPR) ^ col_swz<C>(r);
+    const int tid = threadIdx.x, r = tid / UPR, u = (tid % UPR) ^ col_swz(r);
     voff = u < valid_units ? (uint32_t)r * pitch + u * 16 : kNowhere;
     step = RSTEP * pitch;
   }
@@ -213,13 +215,12 @@ struct ColTile {
 // Fragments of v_mfma_f32_16x16x32_bf16: lane l holds index l % 16 of a 16-wide tile and
 // c = 32 ks + 8 (l / 16) + 0..7 of the stage.  (The 16x16 form: at the card's power limit it ran at
 // 2.1 PFLOP/s on random operands held in registers, the 32x32x16 form at 1.8.)
-template <int KB>
 struct RowFrag {
   uint32_t at[KB / 64];  // per ks
   __device__ __forceinline__ void init(int first) {  // first: a multiple of 16
     const int lane = lane_id(), r = first + (lane & 15), g = lane >> 4;
 #pragma unroll
-    for (int ks = 0; ks < KB / 64; ks++) at[ks] = r * KB + ((4 * ks + g) ^ row_swz<KB>(r)) * 16;
+    for (int ks = 0; ks < KB / 64; ks++) at[ks] = r * KB + ((4 * ks + g) ^ row_swz(r)) * 16;
   }
   __device__ __forceinline__ void read(const uint8_t *tile, int t, int ks, frag8 &f) const {
     f.q = *reinterpret_cast<const uint4 *>(tile + at[ks] + t * 16 * KB);
@@ -240,7 +241,7 @@ struct ColFrag {
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int u = first / 8 + t * 2 + ((i & 3) >> 1);
-      at[t] = c * C * 2 + (u ^ col_swz<C>(c)) * 16 + (i & 1) * 8;
+      at[t] = c * C * 2 + (u ^ col_swz(c)) * 16 + (i & 1) * 8;
     }
   }
   __device__ __forceinline__ void read(const uint8_t *tile, int t, int ks, frag8 &f) const {

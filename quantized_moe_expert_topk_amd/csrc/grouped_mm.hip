@@ -38,20 +38,20 @@ hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
   if (prod == kForward) {
     if (few_rows_faster(a, rows, 2, 0.34)) return launch_few_rows(a, false, out_bf16, s);
-    if (mean > 256) return run_product<kForward, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
-    if (mean > 64) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
-    if (mean > 32) return run_product<kForward, kBf16, 256, 128, 4, 2, 128, 3, true>(a, out_bf16, s);
-    if (mean > 16) return run_product<kForward, kBf16, 128, 64, 2, 2, 128, 3, true>(a, out_bf16, s);
-    return run_product<kForward, kBf16, 128, 32, 4, 1, 128, 3, true>(a, out_bf16, s);
+    if (mean > 256) return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+    if (mean > 64) return run_product<kForward, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
+    if (mean > 32) return run_product<kForward, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
+    if (mean > 16) return run_product<kForward, kBf16, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
+    return run_product<kForward, kBf16, 128, 32, 4, 1, 3, true>(a, out_bf16, s);
   }
   if (prod == kDgrad) {
-    if (mean > 256) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
-    if (mean > 64) return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3>(a, out_bf16, s);
-    return run_product<kDgrad, kBf16, 256, 128, 4, 2, 128, 3, true>(a, out_bf16, s);
+    if (mean > 256) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+    if (mean > 64) return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
+    return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
   }
   if ((long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256)
-    return run_product<kWgrad, kBf16, 256, 256, 2, 4, 128, 2>(a, out_bf16, s);
-  return run_product<kWgrad, kBf16, 128, 128, 2, 2, 128, 2>(a, out_bf16, s);
+    return run_product<kWgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+  return run_product<kWgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
 }
 
 }  // namespace qmoe

@@ -39,40 +39,48 @@ __device__ __forceinline__ void static_for(F &&f) {
 // seen on random codes: 1.1e-4 of the sum of magnitudes; about 3e-5 of the result's norm), far below a
 // bf16 output's own rounding (2^-9) and far above an fp32 one's.  kFp8Exact multiplies the codes as
 // bf16, which holds every e4m3 value and whose MFMA adds in fp32, at half the rate.
+constexpr int kBf16 = 0, kFp8Native = 1, kFp8Exact = 2;
+
 constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
+
 // Cache policy of the output's stores: non-temporal, written through to memory.  Nothing here reads them again,
 // and lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows,
 // N 1024, K 2048: 349 us with the default policy, 278 with the non-temporal hint, 246 with both).
 constexpr int kStorePolicy = 2 | 16;
-constexpr int kBf16 = 0, kFp8Native = 1, kFp8Exact = 2;
 
-template <int PROD, int BP, int BQ, int WP, int WQ, int KB>
+template <int PROD, int BP, int BQ, int WP, int WQ>
 struct ProductTypes {
   static constexpr int THREADS = 64 * WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
   static constexpr bool A_ROWS = PROD == kForward, B_ROWS = PROD != kWgrad;
-  using ATile = std::conditional_t<A_ROWS, RowTile<BP, THREADS, KB>, ColTile<BP, THREADS, KB>>;
-  using BTile = std::conditional_t<B_ROWS, RowTile<BQ, THREADS, KB>, ColTile<BQ, THREADS, KB>>;
-  using AFrag = std::conditional_t<A_ROWS, RowFrag<KB>, ColFrag<BP, TP>>;
-  using BFrag = std::conditional_t<B_ROWS, RowFrag<KB>, ColFrag<BQ, TQ>>;
+  using ATile = std::conditional_t<A_ROWS, RowTile<BP, THREADS>, ColTile<BP, THREADS>>;
+  using BTile = std::conditional_t<B_ROWS, RowTile<BQ, THREADS>, ColTile<BQ, THREADS>>;
+  using AFrag = std::conditional_t<A_ROWS, RowFrag, ColFrag<BP, TP>>;
+  using BFrag = std::conditional_t<B_ROWS, RowFrag, ColFrag<BQ, TQ>>;
 };
 
 // One output tile and the part of the contraction that it sums.
 struct OutTile {
   int e, p0, q0, rows;  // rows: output rows q0, q0 + 1, ... that exist
-  int row0, len;        // wgrad: the expert's rows; len: the contraction's length in `per` units below
+  int row0, len;        // wgrad: the expert's first row; len: the contraction in 16-byte units (forward) or rows
 };
 
-// NT: the weights are loaded with the non-temporal hint, for experts whose rows fill about one row tile: then
-// each weight tile is read by one workgroup only, and the hint keeps it from pushing out the activations.
-// 256 experts, N 1024, K 2048, forward us without / with: m = 2 203 / 184, 64 223 / 198, 128 269 / 243 (dgrad
-// 242 / 217), fp8 m = 2 91 / 79.5; but where several row tiles share the weights 139 / 167 (fp8 8192 x 4096 x
-// 4096).
-// Workgroups are persistent: each takes a sequence of tiles, and its loads run NS stages ahead of its products
-// across the tiles' borders, so that only the first tile waits for its first loads, and a tile's stores
-// leave while the next one's operands arrive.
-template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int KB, int NS, bool NT, int OUT>
+// The tiled product.  What bounds it: large groups run at the card's power limit (8 experts of 2048 rows, N and K
+// 4096: about 1.28 PFLOP/s in each of the three products at 2.0 GHz, the matrix cores busy 97% of a stage's
+// cycles when loads are left out; a library product of the same size reaches 1.2 to 1.56 by layout), small
+// groups by reading the weights (4.0 TB/s at 256 rows an expert, 5.2 at 128, 5.8 at 2).  Choices:
+// - 16 x 16 matrix instructions (RowFrag says why), a wave tile of 64 x 64 to 128 x 64: operands from LDS once
+//   per 64 to 128 columns, and two waves a SIMD.
+// - stages of 128 bytes of c: 64-byte pieces of rows took a third longer to load.
+// - Workgroups are persistent: each takes a sequence of tiles, and its loads run NS stages ahead of its products
+//   across the tiles' borders, so that only the first tile waits for its first loads, and a tile's stores leave
+//   while the next one's operands arrive (256 experts of 256 rows: 370 us one tile a workgroup, 347 so).
+// - NT: the weights are loaded with the non-temporal hint, for experts whose rows fill one row tile: then each
+//   weight tile is read by one workgroup only, and the hint keeps it from pushing out the activations.  256
+//   experts, N 1024, K 2048, forward, us without / with: m = 2 203 / 184, 64 223 / 198, fp8 m = 2 91 / 79.5; but
+//   where several row tiles share the weights 139 / 167 (fp8 8192 x 4096 x 4096).
+template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool NT, int OUT>
 __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
-  using T = ProductTypes<PROD, BP, BQ, WP, WQ, KB>;
+  using T = ProductTypes<PROD, BP, BQ, WP, WQ>;
   constexpr bool FP8 = DT != kBf16, OUT_BF16 = OUT == kOutBf16;
   constexpr int TP = T::TP, TQ = T::TQ;
   constexpr int XS_BYTES = FP8 ? 4 * (BQ > 64 ? BQ : 64) : 0, SCALES = FP8 ? XS_BYTES + 256 : 0;
@@ -94,15 +102,15 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   if constexpr (PROD == kWgrad) {
     q_total = a.g.E * a.q_tiles;
   } else if (a.g.offsets) {
-    make_tile_table<T::THREADS>(a.g, BQ, first);
-    q_total = __builtin_amdgcn_readfirstlane(first[a.g.E]);
+    q_total = make_tile_table<T::THREADS>(a.g, BQ, first);
   } else {
     q_total = (a.g.M + BQ - 1) / BQ;
   }
   constexpr int PER = PROD == kForward ? KB / 16 : KB / 2;  // 16-byte units, or rows, of a stage
 
   // Workgroup L runs on XCD L mod 8: of each round of gridDim.x tiles, an XCD takes a run of consecutive ones.
-  // The order is q_run (4, if there are as many) q tiles, then the next p: a run covers a block, which reads the fewest operand rows.
+  // The order is q_run (4, if there are as many) q tiles, then the next p: a run covers a block, which reads the
+  // fewest operand rows.
   // Moves t on to the next tile that exists, from t itself; false past the last one.
   auto locate = [&](int &t, OutTile &o) __attribute__((always_inline)) {
     const int band = a.q_run * a.p_tiles;
@@ -243,7 +251,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   };
   // Asks for lines of the stage after the next one, so that they are in this XCD's L2 when its loads go out:
   // LDS has room for one stage of 256 x 256 ahead only, less than memory's latency.  The 4 q tiles that share an
-  // A panel, and 8 p tiles that share a B panel, each touch their part of it (4 bytes of every line).
+  // A panel, and 8 p tiles that share a B panel, each touch their part of it (4 bytes of every line).  The loads
+  // alone of 8 experts of 2048 rows, N and K 4096, take 377 us without and 293 with it; gradients of 256 experts
+  // of 128 rows went from 667 to 620 us when it reached across tiles.
   const int t0 = blockIdx.x / 8;  // (the place in the XCD's run)
   const int wn = wave == 0 ? (lane * 4 + t0 % 4) : (lane * 8 + t0 / 4 % 8) & 255;  // line of the panel's 256
   const bool wrow = wave == 0 ? T::A_ROWS : T::B_ROWS;
@@ -326,7 +336,6 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   auto multiply = [&](int from, int i) __attribute__((always_inline)) {
     acc[i / TQ][i % TQ] = mfma_bf16(af[from][i / TQ], bf[from][i % TQ], acc[i / TQ][i % TQ]);
   };
-  static_assert(DT != kBf16 || NKS % 2 == 0, "the fragment sets alternate within a stage");
   auto stage = [&]() __attribute__((always_inline)) {
     const int next = slot == NS - 1 ? 0 : slot + 1;
     static_for<NKS>([&](auto ks) __attribute__((always_inline)) {
@@ -360,8 +369,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   };
 
   // fp8: a stage is one block of 128; its products go to a zero accumulator, scaled into the sum.
-  constexpr int WB = TP * 16 / 128 > 0 ? TP * 16 / 128 : 1;
-  static_assert(!FP8 || (KB == 128 && WB == 1 && (TP * 16 == 128 || 128 % (TP * 16) == 0)), "one weight scale a wave");
+  static_assert(!FP8 || 128 % (TP * 16) == 0, "one weight scale a wave and stage");
   auto read_scales = [&](int sl, float (&sx)[TQ]) __attribute__((always_inline)) {
     const float *t = reinterpret_cast<const float *>(lds + sl * STAGE + T::ATile::kBytes + T::BTile::kBytes);
     const float sw = t[XS_BYTES / 4 + wp * TP * 16 / 128];
@@ -562,7 +570,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
   wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
 }
 
-template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int KB, int NS, bool NT = false>
+template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool NT = false>
 hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   const int P = PROD == kForward ? a.N : a.K;
   a.p_tiles = (P + BP - 1) / BP;
@@ -580,7 +588,7 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 3 : 1);
   const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
   const auto launch = [&](auto out) {
-    k_product<PROD, DT, BP, BQ, WP, WQ, KB, NS, NT, decltype(out)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
+    k_product<PROD, DT, BP, BQ, WP, WQ, NS, NT, decltype(out)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
   };
   if (out_bf16)
     launch(std::integral_constant<int, kOutBf16>{});

@@ -417,6 +417,29 @@ def test_bad_ranges_stay_inside():
         check_fp8("bad ranges", fbuf[300:300 + M][r], dequant_rows(xq[r], xs[:, r]), dequant_weights(wq[e], ws[e]), "ints")
 
 
+@pytest.mark.parametrize("E,M", [(1024, 5000), (7, 300)])
+def test_overlapping_ranges_end(E, M):
+    """Every expert claims every row: the outputs are undefined, but the calls end, write rows of the matrix only,
+    and a call with proper ranges after them is right."""
+    N, K = 72, 80
+    g = gen(9)
+    x, w = ints(g, M, K), ints(g, E, N, K)
+    xq, xs = fp8_rows(g, M, K, "ints")
+    wq, ws = fp8_weights(g, E, N, K, "ints")
+    off = torch.zeros(E, dtype=torch.int32, device=DEV)
+    cnt = torch.full((E,), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    for hint in (1, M):  # the kernel for few rows and a tiled one
+        buf = torch.full((M + 600, N), 7.0, device=DEV)
+        qm.moe_grouped_mm(x, w, off, cnt, hint, out=buf[300:300 + M])
+        qm.moe_grouped_block_mm(xq, xs, wq, ws, off, cnt, hint, out=buf[300:300 + M])
+        torch.cuda.synchronize()
+        assert bool((buf[:300] == 7).all()) and bool((buf[300 + M:] == 7).all())
+    cnt.zero_()
+    cnt[E - 1] = M
+    y = qm.moe_grouped_mm(x, w, off, cnt, out_dtype=torch.float32)
+    assert torch.equal(y.double(), x.double() @ w[E - 1].double().t())
+
+
 def test_matrices_past_4_gib():
     """Weights, gradients and rows whose byte offsets need more than 32 bits."""
     E, N, K = 260, 4104, 2056  # 4.4 GB of bf16 weights, 8.8 GB of fp32 gradient
