@@ -30,22 +30,23 @@ bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
 //   m = 64                                               198                                              221     188
 //   m = 2                                                              184                                191     161
 // Groups are ragged: the hint is given where the mean is half a row tile at most, so that few experts need a
-// second one (gradients of 256 experts of 128 +- 90 rows, us: 742 with it, 668 without).  256 x 256 for large
-// groups (8 experts of 2048 rows, N and K 4096: 428 against 484).
+// second one (gradients of 256 experts of 128 +- 90 rows, us: 742 with it, 668 without), and 256 x 256, whose
+// last row tile is half empty on average, from a mean of 512 (forward, 256 experts of 256 +- 250 rows: 437
+// against 365; 8 experts of 2048 rows, N and K 4096: 428 against 484).
 // wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 236 against 262 for 256 x 128 and 293 for
 // 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs.
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
   if (prod == kForward) {
     if (few_rows_faster(a, rows, 2, 0.34)) return launch_few_rows(a, false, out_bf16, s);
-    if (mean > 256) return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+    if (mean > 512) return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
     if (mean > 64) return run_product<kForward, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
     if (mean > 32) return run_product<kForward, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
     if (mean > 16) return run_product<kForward, kBf16, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
     return run_product<kForward, kBf16, 128, 32, 4, 1, 3, true>(a, out_bf16, s);
   }
   if (prod == kDgrad) {
-    if (mean > 256) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+    if (mean > 512) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
     if (mean > 64) return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
     return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
   }

@@ -75,6 +75,7 @@ COUNTS = {
     "long": [700, 0, 513],
     "many": [((7 * i) % 5) for i in range(130)],
     "wide": [300, 257, 255, 256],
+    "huge": [1300, 0, 900],
     # enough experts for each tile that the launchers pick by the mean number of rows
     "mean 12": [((5 * i) % 25) for i in range(130)],
     "mean 24": [((7 * i) % 49) for i in range(130)],
