@@ -43,11 +43,13 @@ int check_out(const char *fn, int out_dtype) {
   return MOE_OK;
 }
 
-int check_groups(const char *fn, const int32_t *offsets, int E, int M, int expected_rows) {
+int check_groups(const char *fn, const int32_t *offsets, const int32_t *counts, int E, int M, int expected_rows) {
   if (!offsets) return abi_fail(MOE_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
   if (E < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: E=%d must be positive", fn, E);
   if (int rc = check_rows(fn, M)) return rc;
   if (E > 1024) return abi_fail(MOE_ERR_UNSUPPORTED, "%s: E=%d > 1024", fn, E);
+  if (misaligned(offsets, 4) || misaligned(counts, 4))
+    return abi_fail(MOE_ERR_INVALID_ARG, "%s: offsets and counts must be 4-byte aligned", fn);
   if (expected_rows < 0) return abi_fail(MOE_ERR_INVALID_ARG, "%s: expected_rows=%d is negative", fn, expected_rows);
   return MOE_OK;
 }
@@ -75,7 +77,7 @@ int rows_hint(int expected_rows, int M) { return expected_rows > 0 ? std::min(ex
 // One of the three bf16 products.  a: dy or x rows, b: the weights, or x rows for wgrad.
 int grouped(const char *fn, int prod, const void *a, const void *b, const int32_t *offsets, const int32_t *counts,
             int E, int M, int expected_rows, int N, int K, void *out, int out_dtype, int accumulate, void *stream) {
-  if (int rc = check_groups(fn, offsets, E, M, expected_rows)) return rc;
+  if (int rc = check_groups(fn, offsets, counts, E, M, expected_rows)) return rc;
   if (N < 1 || K < 1) return abi_fail(MOE_ERR_INVALID_ARG, "%s: N=%d K=%d must be positive", fn, N, K);
   if (N % 8 || K % 8)
     return abi_fail(MOE_ERR_UNSUPPORTED, "%s: N=%d and K=%d must be multiples of 8 (16-byte loads)", fn, N, K);
@@ -89,7 +91,8 @@ int grouped(const char *fn, int prod, const void *a, const void *b, const int32_
   const Range ra{a, prod == kForward ? bytes_k : bytes_n};
   const Range rb{b, prod == kWgrad ? bytes_k : M ? bytes_w * 2 : 0};
   const Range ro{out, (prod == kForward ? rows * N : prod == kDgrad ? rows * K : bytes_w) * es};
-  if (int rc = check_inputs(fn, {ra, rb}, ro, 16)) return rc;
+  const Range ri{offsets, ((size_t)E + (counts ? 0 : 1)) * 4}, rc_{counts, counts ? (size_t)E * 4 : 0};
+  if (int rc = check_inputs(fn, {ra, rb, ri, rc_}, ro, 16)) return rc;
   if (int rc = check_aligned16(fn, {a, b})) return rc;
   if (M == 0 && (prod != kWgrad || accumulate)) return abi_ok();
   if (int rc = abi_check_device()) return rc;
@@ -122,7 +125,9 @@ int block(const char *fn, const void *xq, const float *xs, const void *wq, const
                KB = ((size_t)K + 127) / 128;
   const Range ro{out, rows * N * es};
   if (int rc = check_inputs(fn, {{xq, rows * K}, {xs, rows * KB * 4}, {wq, M ? (size_t)E * N * K : 0},
-                                 {ws, M ? E * NB * KB * 4 : 0}}, ro, 16))
+                                 {ws, M ? E * NB * KB * 4 : 0},
+                                 {offsets, offsets ? ((size_t)E + (counts ? 0 : 1)) * 4 : 0},
+                                 {counts, counts ? (size_t)E * 4 : 0}}, ro, 16))
     return rc;
   if (int rc = check_aligned16(fn, {xq, wq})) return rc;
   if (misaligned(xs, 4) || misaligned(ws, 4))
@@ -191,7 +196,7 @@ int moe_block_mm(const void *xq, const float *xs, const void *wq, const float *w
 int moe_grouped_block_mm(const void *xq, const float *xs, const void *wq, const float *ws, int layout,
                          const int32_t *offsets, const int32_t *counts, int E, int M, int expected_rows, int N, int K,
                          void *y, int out_dtype, void *stream) {
-  if (int rc = check_groups("moe_grouped_block_mm", offsets, E, M, expected_rows)) return rc;
+  if (int rc = check_groups("moe_grouped_block_mm", offsets, counts, E, M, expected_rows)) return rc;
   return block("moe_grouped_block_mm", xq, xs, wq, ws, layout, offsets, counts, E, M, expected_rows, N, K, y,
                out_dtype, stream);
 }

@@ -144,6 +144,7 @@ struct ProductArgs {
   int tile16;      // fp8: the weights are in MOE_LAYOUT_TILE16
   int accumulate;  // wgrad: add to out
   int p_tiles, q_tiles, q_run;  // set by the launcher: tiles of the output, and q tiles taken before the next p
+  int write_through;  // set by the launcher: store policy
 };
 
 // rows: about how many rows all groups hold together; it picks the kernel, never the result's meaning.

@@ -43,10 +43,12 @@ constexpr int kBf16 = 0, kFp8Native = 1, kFp8Exact = 2;
 
 constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
 
-// Cache policy of the output's stores: non-temporal, written through to memory.  Nothing here reads them again,
-// and lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows,
-// N 1024, K 2048: 349 us with the default policy, 278 with the non-temporal hint, 246 with both).
-constexpr int kStorePolicy = 2 | 16;
+// Cache policy of the stores of large outputs: non-temporal, written through to memory.  Nothing here reads them
+// again, and lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows,
+// N 1024, K 2048: 349 us with the default policy, 278 with the non-temporal hint, 246 with both).  Outputs that L2
+// can hold keep the default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.
+constexpr int kWriteThrough = 2 | 16;
+constexpr double kThroughBytes = 16e6;
 
 template <int PROD, int BP, int BQ, int WP, int WQ>
 struct ProductTypes {
@@ -488,6 +490,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
         }
       }
     }
+    const auto put = [&](auto policy) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < TQ; q++) {
       const uint32_t row = (wq * TQ * 16 + q * 16 + (lane & 15)) * pitch;
@@ -506,14 +509,14 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
             const auto hi = __builtin_amdgcn_permlane16_swap(h[0][1], h[1][1], false, false);
             const int c = c0 + (p + (g & 1)) * 16 + 8 * (g >> 1);
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro,
-                                                   (int)(c < P ? row + c * OS : kNowhere), 0, kStorePolicy);
+                                                   (int)(c < P ? row + c * OS : kNowhere), 0, policy());
           }
         } else {
 #pragma unroll
           for (int p = 0; p < TP; p++) {
             const int c = c0 + p * 16 + 4 * g;
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[p][q]), ro,
-                                                   (int)(c < P ? row + c * OS : kNowhere), 0, kStorePolicy);
+                                                   (int)(c < P ? row + c * OS : kNowhere), 0, policy());
           }
         }
       } else {
@@ -530,6 +533,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
           }
       }
     }
+    };
+    // (256 x 256 tiles are for large outputs, and have no registers for the choice)
+    if (BQ == 256 || a.write_through)
+      put(std::integral_constant<int, kWriteThrough>{});
+    else
+      put(std::integral_constant<int, 0>{});
     stored = P % (OUT_BF16 ? 8 : 4) == 0;
   };
 
@@ -582,6 +591,8 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
     q = a.g.offsets ? a.g.M / BQ + std::min(a.g.E, a.g.M) : (a.g.M + BQ - 1) / BQ;
   }
   a.q_run = (int)std::max(1LL, std::min(4LL, q));
+  const double out_bytes = (double)(PROD == kWgrad ? (long long)a.g.E * a.N : a.g.M) * P * (out_bf16 ? 2 : 4);
+  a.write_through = out_bytes > kThroughBytes;
   const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
   if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
   constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) + 256 : 0)) + kMaxExperts * 4 + 512;

@@ -43,6 +43,9 @@ REFUSED = [
     (PRODUCTS, dict(b=None), L.MOE_ERR_INVALID_ARG),
     (EVERY, dict(out=None), L.MOE_ERR_INVALID_ARG),
     (GROUPED, dict(off=None), L.MOE_ERR_INVALID_ARG),
+    (GROUPED, dict(off=ctypes.c_void_p((3 << 40) + 2)), L.MOE_ERR_INVALID_ARG),
+    (GROUPED, dict(cnt=ctypes.c_void_p((7 << 40) + 1)), L.MOE_ERR_INVALID_ARG),
+    (GROUPED, dict(cnt=at(4)), L.MOE_ERR_INVALID_ARG),  # the output over the counts
     (GROUPED, dict(E=0), L.MOE_ERR_INVALID_ARG),
     (GROUPED, dict(E=1025), L.MOE_ERR_UNSUPPORTED),
     (GROUPED, dict(rows=-1), L.MOE_ERR_INVALID_ARG),
