@@ -33,6 +33,9 @@ bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
 // second one (gradients of 256 experts of 128 +- 90 rows, us: 742 with it, 668 without), and 256 x 256, whose
 // last row tile is half empty on average, from a mean of 512 (forward, 256 experts of 256 +- 250 rows: 437
 // against 365; 8 experts of 2048 rows, N and K 4096: 428 against 484).
+// Few tiles: smaller ones, and for a handful six stages in LDS, since a stage then takes a part of memory's latency
+// (dgrad, us: 6 rows of 5 experts, 3648 x 64, 40 with 256 x 128 and 24 with 128 x 32; 20 rows, 1912 x 728, 31 and
+// 18; 16 experts of 757 rows, 2632 x 216, 69 with 256 x 256 and 40 with 128 x 128).
 // wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 236 against 262 for 256 x 128 and 293 for
 // 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs.
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
@@ -45,12 +48,17 @@ hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_
     if (mean > 16) return run_product<kForward, kBf16, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
     return run_product<kForward, kBf16, 128, 32, 4, 1, 3, true>(a, out_bf16, s);
   }
+  const auto q_tiles = [&](int bq) { return (long long)rows / bq + std::min(a.g.E, rows); };  // about
+  const auto p_tiles = [&](int bp) { return (a.K + bp - 1LL) / bp; };
   if (prod == kDgrad) {
+    if (q_tiles(32) * p_tiles(128) <= 256) return run_product<kDgrad, kBf16, 128, 32, 4, 1, 6>(a, out_bf16, s);
+    if (q_tiles(mean > 512 ? 256 : 128) * p_tiles(256) < 256)
+      return run_product<kDgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
     if (mean > 512) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
     if (mean > 64) return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
     return run_product<kDgrad, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
   }
-  if ((long long)a.g.E * ((a.N + 255) / 256) * ((a.K + 255) / 256) >= 256)
+  if (a.g.E * ((a.N + 255LL) / 256) * p_tiles(256) >= 256)
     return run_product<kWgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
   return run_product<kWgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
 }

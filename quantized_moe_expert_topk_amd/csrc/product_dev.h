@@ -46,7 +46,9 @@ constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
 // Cache policy of the stores of large outputs: non-temporal, written through to memory.  Nothing here reads them
 // again, and lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows,
 // N 1024, K 2048: 349 us with the default policy, 278 with the non-temporal hint, 246 with both).  Outputs that L2
-// can hold keep the default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.
+// can hold keep the default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.  And rows that
+// end inside a 128-byte line do: their part lines went to memory one by one (wgrad of 60 experts, 1912 x 728: 159 us
+// written through, 33 not).
 constexpr int kWriteThrough = 2 | 16;
 constexpr double kThroughBytes = 16e6;
 
@@ -80,8 +82,8 @@ struct OutTile {
 //   weight tile is read by one workgroup only, and the hint keeps it from pushing out the activations.  256
 //   experts, N 1024, K 2048, forward, us without / with: m = 2 203 / 184, 64 223 / 198, fp8 m = 2 91 / 79.5; but
 //   where several row tiles share the weights 139 / 167 (fp8 8192 x 4096 x 4096).
-template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool NT, int OUT>
-__global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
+template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool NT, int OUT, bool THROUGH>
+__global__ __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && NS * (BP + BQ) * KB > 81920 ? 1 : 2) void k_product(ProductArgs a) {
   using T = ProductTypes<PROD, BP, BQ, WP, WQ>;
   constexpr bool FP8 = DT != kBf16, OUT_BF16 = OUT == kOutBf16;
   constexpr int TP = T::TP, TQ = T::TQ;
@@ -534,11 +536,20 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_product(ProductArgs a) {
       }
     }
     };
-    // (256 x 256 tiles are for large outputs, and have no registers for the choice)
-    if (BQ == 256 || a.write_through)
-      put(std::integral_constant<int, kWriteThrough>{});
-    else
-      put(std::integral_constant<int, 0>{});
+    // (256 x 256 tiles have no registers for the choice: there it is made when the kernel is launched)
+    const auto through = [&]() __attribute__((always_inline)) { put(std::integral_constant<int, kWriteThrough>{}); };
+    const auto plain = [&]() __attribute__((always_inline)) { put(std::integral_constant<int, 0>{}); };
+    if constexpr (BQ == 256) {
+      if constexpr (THROUGH)
+        through();
+      else
+        plain();
+    } else {
+      if (a.write_through)
+        through();
+      else
+        plain();
+    }
     stored = P % (OUT_BF16 ? 8 : 4) == 0;
   };
 
@@ -592,14 +603,18 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   }
   a.q_run = (int)std::max(1LL, std::min(4LL, q));
   const double out_bytes = (double)(PROD == kWgrad ? (long long)a.g.E * a.N : a.g.M) * P * (out_bf16 ? 2 : 4);
-  a.write_through = out_bytes > kThroughBytes;
+  a.write_through = out_bytes > kThroughBytes && (long long)P * (out_bf16 ? 2 : 4) % 128 == 0;
   const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
   if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
   constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) + 256 : 0)) + kMaxExperts * 4 + 512;
   constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 3 : 1);
   const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
   const auto launch = [&](auto out) {
-    k_product<PROD, DT, BP, BQ, WP, WQ, NS, NT, decltype(out)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
+    constexpr int OUT = decltype(out)::value;
+    if (BQ == 256 && !a.write_through)
+      k_product<PROD, DT, BP, BQ, WP, WQ, NS, NT, OUT, BQ != 256><<<grid, 64 * WP * WQ, 0, s>>>(a);
+    else
+      k_product<PROD, DT, BP, BQ, WP, WQ, NS, NT, OUT, true><<<grid, 64 * WP * WQ, 0, s>>>(a);
   };
   if (out_bf16)
     launch(std::integral_constant<int, kOutBf16>{});
