@@ -24,6 +24,7 @@ hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStr
   if (mean <= (out_bf16 && wide >= 128 ? 32 : 64))
     return run_product<kForward, kFp8Exact, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
   if (!out_bf16) return run_product<kForward, kFp8Exact, 128, 128, 2, 2, 2>(a, out_bf16, s);
+  if (wide < 64) return run_product<kForward, kFp8Native, 128, 128, 2, 4, 3>(a, out_bf16, s);
   if (wide < 128) return run_product<kForward, kFp8Native, 128, 128, 2, 2, 2>(a, out_bf16, s);
   if (mean <= 64) return run_product<kForward, kFp8Native, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
   return run_product<kForward, kFp8Native, 256, 128, 4, 2, 3>(a, out_bf16, s);

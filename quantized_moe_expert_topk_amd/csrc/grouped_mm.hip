@@ -60,6 +60,8 @@ hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_
   }
   if (a.g.E * ((a.N + 255LL) / 256) * p_tiles(256) >= 256)
     return run_product<kWgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+  if (a.g.E * ((a.N + 127LL) / 128) * p_tiles(128) <= 256)
+    return run_product<kWgrad, kBf16, 128, 128, 4, 2, 3>(a, out_bf16, s);
   return run_product<kWgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
 }
 
