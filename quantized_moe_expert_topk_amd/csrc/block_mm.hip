@@ -13,7 +13,9 @@ namespace qmoe {
 //   m = 24                                                                                  98          88
 //   m = 2                                                                       100         91          79
 // Large groups: fp8 256 x 128 317 against 335 for 128 x 128 (8 experts of 2048 rows, N and K 4096), one of
-// 8192 rows 142 against 150; with fewer tiles than half the CUs, the smaller ones.
+// 8192 rows 142 against 150; with fewer tiles than half the CUs, the smaller ones, and with fewer than a quarter
+// their eight-wave form with three stages (588 rows, 1320 x 6768: 36 against 52 for the two-stage one of four waves;
+// 256 rows, 4096 x 4096: 22 and 26; 512 rows, 2048 x 2048: 14 and 16).
 hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
   const long long wide = (a.g.offsets ? rows / 128 + std::min(a.g.E, rows) : (rows + 127) / 128) * ((a.N + 255LL) / 256);

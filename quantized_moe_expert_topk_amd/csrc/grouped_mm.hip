@@ -37,7 +37,9 @@ bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
 // (dgrad, us: 6 rows of 5 experts, 3648 x 64, 40 with 256 x 128 and 24 with 128 x 32; 20 rows, 1912 x 728, 31 and
 // 18; 16 experts of 757 rows, 2632 x 216, 69 with 256 x 256 and 40 with 128 x 128).
 // wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 236 against 262 for 256 x 128 and 293 for
-// 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs.
+// 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs; a tile of 128 x 128 for each CU at most
+// takes eight waves and three stages (4 experts of 6546 rows, 64 x 1440: 53 against 70 for four waves and two stages;
+// 8 of 25 rows, 264 x 200: 5.2 and 5.1).
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
   if (prod == kForward) {
