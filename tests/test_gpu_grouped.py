@@ -81,8 +81,10 @@ COUNTS = {
     "mean 24": [((7 * i) % 49) for i in range(130)],
     "mean 48": [((11 * i) % 97) for i in range(130)],
     "mean 80": [((13 * i) % 161) for i in range(130)],
+    "forty": [((13 * i) % 151) for i in range(40)],  # fewer tiles than CUs, but not few
 }
-SIZES = [(8, 8), (64, 64), (136, 72), (264, 200), (256, 512), (520, 1032)]  # (N, K)
+SIZES = [(8, 8), (64, 64), (136, 72), (264, 200), (256, 512), (520, 1032),
+         (1024, 512)]  # (N, K); the last: rows of whole lines, of outputs too large for L2
 
 
 @pytest.mark.parametrize("NK", SIZES, ids=str)
@@ -90,8 +92,8 @@ SIZES = [(8, 8), (64, 64), (136, 72), (264, 200), (256, 512), (520, 1032)]  # (N
 def test_forward_and_gradients(counts, NK):
     """All three products on integer-valued inputs (exact in fp32) and on normal ones (bound)."""
     N, K = NK
-    if counts.startswith("mean") and N * K not in (264 * 200, 520 * 1032):
-        pytest.skip("many experts at two sizes are enough")
+    if counts.startswith("mean") and NK not in ((264, 200), (520, 1032), (1024, 512)):
+        pytest.skip("many experts at three sizes are enough")
     off, cnt, M = ranges(COUNTS[counts])
     E = len(COUNTS[counts])
     g = gen(len(counts) * 1000 + N + K)
@@ -203,7 +205,7 @@ def check_fp8(name, got, X, W, kind):
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 1024, 2048), (3, 1, 128), (17, 130, 144), (33, 257, 400), (64, 64, 64),
                                    (100, 384, 1040), (129, 515, 256), (256, 256, 512), (300, 1000, 272),
-                                   (513, 128, 8208)])
+                                   (513, 128, 8208), (1000, 2050, 272), (2000, 2064, 144), (2100, 4096, 272)])
 def test_block_mm(M, N, K):
     g = gen(M + N + K)
     for kind in ("ints", "normal"):
@@ -243,6 +245,21 @@ def test_grouped_block_mm(counts, N, K):
                     idle[r] = False
                     check_fp8(f"{kind} {layout} {e}", out[:M][r], dequant_rows(xq[r], xs[:, r]), dequant_weights(wq[e], ws[e]), kind)
                 assert bool((out[idle] == 7).all())
+
+
+@pytest.mark.parametrize("N,K", [(131, 144), (144, 272), (1024, 272), (1040, 128)])
+@pytest.mark.parametrize("counts", ["ragged", "wide", "mean 24", "mean 48", "mean 80", "forty"])
+def test_grouped_block_mm_bf16(counts, N, K):
+    off, cnt, M = ranges(COUNTS[counts])
+    E, g = len(COUNTS[counts]), gen(N + K + M)
+    for kind in ("ints", "normal"):
+        xq, xs = fp8_rows(g, M, K, kind)
+        wq, ws = fp8_weights(g, E, N, K, kind)
+        print(f"[grouped_block_mm] {counts} {N} {K} {kind} bf16", flush=True)
+        y = qm.moe_grouped_block_mm(xq, xs, wq, ws, off, out_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        for e, r in enumerate(rows_of(off, cnt)):
+            check_fp8(f"{kind} {e}", y[r], dequant_rows(xq[r], xs[:, r]), dequant_weights(wq[e], ws[e]), kind)
 
 
 # --------------------------------------------------------------------------------------- quantiser
@@ -348,7 +365,7 @@ def test_gradients_against_differences():
     assert float((lin * c["dy"].double()).sum()) == float((dw.double() * dW.double()).sum())
 
 
-@pytest.mark.parametrize("E,N,K", [(6, 264, 392), (130, 520, 1032)])
+@pytest.mark.parametrize("E,N,K", [(6, 264, 392), (40, 264, 392), (130, 520, 1032), (130, 256, 1024)])
 def test_wgrad_accumulates(E, N, K):
     c = ragged(3, N, K, [(17 * i) % 40 for i in range(E)])
     base = ints(gen(4), E, N, K).float()
