@@ -35,25 +35,34 @@ bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us) {
 // against 365; 8 experts of 2048 rows, N and K 4096: 428 against 484).
 // Few tiles: smaller ones, and for a handful six stages in LDS, since a stage then takes a part of memory's latency
 // (dgrad, us: 6 rows of 5 experts, 3648 x 64, 40 with 256 x 128 and 24 with 128 x 32; 20 rows, 1912 x 728, 31 and
-// 18; 16 experts of 757 rows, 2632 x 216, 69 with 256 x 256 and 40 with 128 x 128).
+// 18; 16 experts of 757 rows, 2632 x 216, 69 with 256 x 256 and 40 with 128 x 128; 16 of 87 rows, 1024 x 1024,
+// 17 with four waves on 128 x 128 and 15.4 with eight).  Forward takes 128 x 128 with eight waves and three stages where
+// a tile for each CU is enough (us against 256 x 128: 2048 rows of 4 experts, 1024 x 4096, 34 and 49; 1400 of 16, 1024 x
+// 1024, 15 and 18; 200 of 2, 1024 x 4096, 29 and 46; with 333 tiles, 3748 of 8, 1120 x 3768, it would be 77 and 63),
+// and 256 x 256 from where 256 x 128 would need a second round (5000 of 4, 1024 x 2048, 92 tiles: 47 and 31; 6000
+// of 4, 2048 x 1024, 224 tiles: 33 and 35).
 // wgrad has E * N * K outputs whatever the rows: 256 x 256 (m = 128: 236 against 262 for 256 x 128 and 293 for
 // 128 x 128; m = 256: 435, 586, 709), unless those are fewer tiles than CUs; a tile of 128 x 128 for each CU at most
 // takes eight waves and three stages (4 experts of 6546 rows, 64 x 1440: 53 against 70 for four waves and two stages;
 // 8 of 25 rows, 264 x 200: 5.2 and 5.1).
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s) {
   const int mean = rows / std::max(1, std::min(a.g.E, rows));
+  const auto q_tiles = [&](int bq) { return (long long)rows / bq + std::min(a.g.E, rows); };  // about
   if (prod == kForward) {
     if (few_rows_faster(a, rows, 2, 0.34)) return launch_few_rows(a, false, out_bf16, s);
-    if (mean > 512) return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
+    if (mean > 64 && q_tiles(128) * ((a.N + 127LL) / 128) <= 256)
+      return run_product<kForward, kBf16, 128, 128, 2, 4, 3>(a, out_bf16, s);
+    if (mean > 512 && q_tiles(256) * ((a.N + 255LL) / 256) > 128)
+      return run_product<kForward, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
     if (mean > 64) return run_product<kForward, kBf16, 256, 128, 4, 2, 3>(a, out_bf16, s);
     if (mean > 32) return run_product<kForward, kBf16, 256, 128, 4, 2, 3, true>(a, out_bf16, s);
     if (mean > 16) return run_product<kForward, kBf16, 128, 64, 2, 2, 3, true>(a, out_bf16, s);
     return run_product<kForward, kBf16, 128, 32, 4, 1, 3, true>(a, out_bf16, s);
   }
-  const auto q_tiles = [&](int bq) { return (long long)rows / bq + std::min(a.g.E, rows); };  // about
   const auto p_tiles = [&](int bp) { return (a.K + bp - 1LL) / bp; };
   if (prod == kDgrad) {
     if (q_tiles(32) * p_tiles(128) <= 256) return run_product<kDgrad, kBf16, 128, 32, 4, 1, 6>(a, out_bf16, s);
+    if (q_tiles(128) * p_tiles(128) <= 256) return run_product<kDgrad, kBf16, 128, 128, 4, 2, 3>(a, out_bf16, s);
     if (q_tiles(mean > 512 ? 256 : 128) * p_tiles(256) < 256)
       return run_product<kDgrad, kBf16, 128, 128, 2, 2, 2>(a, out_bf16, s);
     if (mean > 512) return run_product<kDgrad, kBf16, 256, 256, 2, 4, 2>(a, out_bf16, s);
