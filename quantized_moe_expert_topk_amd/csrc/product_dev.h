@@ -11,17 +11,6 @@
 
 namespace qmoe {
 
-// v_mfma_f32_16x16x128_f8f6f4 with both operands e4m3 and no block scales: lane l holds index l % 16 and
-// 32 bytes of c for its group l / 16 (any 32, as long as both operands take the same).
-__device__ __forceinline__ f32x4_t mfma_e4m3(const frag8 &a0, const frag8 &a1, const frag8 &b0, const frag8 &b1,
-                                             f32x4_t c) {
-  const i32x8_t a = {(int)a0.u[0], (int)a0.u[1], (int)a0.u[2], (int)a0.u[3],
-                     (int)a1.u[0], (int)a1.u[1], (int)a1.u[2], (int)a1.u[3]};
-  const i32x8_t b = {(int)b0.u[0], (int)b0.u[1], (int)b0.u[2], (int)b0.u[3],
-                     (int)b1.u[0], (int)b1.u[1], (int)b1.u[2], (int)b1.u[3]};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
 // f(0), ..., f(N - 1) with compile-time indices (register arrays need them; the unroller gives up on long loops).
 template <class F, int... I>
 __device__ __forceinline__ void static_for_seq(F &&f, std::integer_sequence<int, I...>) {
@@ -32,14 +21,12 @@ __device__ __forceinline__ void static_for(F &&f) {
   static_for_seq(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
-// Operand types.  kFp8Native multiplies e4m3 in the fp8 MFMA, whose sums are not fp32 throughout: as
-// measured with one product at 2^16 and another at 2^(16 - j), products of the same 8 consecutive c
-// are added with what lies below 2^-13 of the largest cut off; across those groups, and with the
-// accumulator, the sum is fp32.  The error is below 7 * 2^-13 of each group's largest product (worst
-// seen on random codes: 1.1e-4 of the sum of magnitudes; about 3e-5 of the result's norm), far below a
-// bf16 output's own rounding (2^-9) and far above an fp32 one's.  kFp8Exact multiplies the codes as
-// bf16, which holds every e4m3 value and whose MFMA adds in fp32, at half the rate.
-constexpr int kBf16 = 0, kFp8Native = 1, kFp8Exact = 2;
+// Operand types.  kFp8: e4m3 codes, multiplied as bf16, which holds every e4m3 value exactly, in the bf16 MFMA, whose
+// sums are fp32.  The fp8 matrix instructions have twice its rate, but not fp32 sums: both v_mfma_f32_16x16x32_fp8_fp8
+// and the 16x16x128 f8f6f4 form add the products of the same 8 consecutive c with what lies below 2^-13 of the
+// largest cut off (one product at 2^16, its negative and one at 2^(16 - j): kept up to j = 13, bf16 up to 24), so a sum
+// that cancels can lose all of what is left.
+constexpr int kBf16 = 0, kFp8 = 1;
 
 constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
 
@@ -381,60 +368,6 @@ __global__ __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && NS * (BP + BQ) * KB >
     for (int q = 0; q < TQ; q++) sx[q] = t[wq * TQ * 16 + q * 16 + (lane & 15)] * sw;
   };
 
-  // In the fp8 matrix cores: as stage(), with the B operand of a whole stage and one p tile of A at a time in
-  // registers.  Before the last two p tiles the slot has been read, so the barrier comes there, and the next
-  // stage's operands are read between their products, B as the last products release its registers.
-  frag8 a8[3][2], b8[TQ][2];
-  float s8[TQ];
-  auto stage_native = [&]() __attribute__((always_inline)) {
-    static_assert(DT != kFp8Native || TP >= 4, "p tiles before and after the barrier");
-    const int next = slot == NS - 1 ? 0 : slot + 1;
-    const uint8_t *ta = lds + slot * STAGE, *na = lds + next * STAGE, *nb = na + T::ATile::kBytes;
-    constexpr auto buf = [](int p) { return p == TP - 1 ? 2 : p & 1; };
-    f32x4_t t[2];
-    static_for<TP>([&](auto p) __attribute__((always_inline)) {
-      if constexpr (p == TP - 2) {
-        wait_loads();
-        barrier_only();
-        open();
-      }
-      static_for<TQ>([&](auto q) __attribute__((always_inline)) {
-        constexpr int i = p * TQ + q;
-        t[i & 1] = mfma_e4m3(a8[buf(p)][0], a8[buf(p)][1], b8[q][0], b8[q][1], zero4());
-        if constexpr (i > 0) {  // the product before, while this one runs
-          constexpr int lp = (i - 1) / TQ, lq = (i - 1) % TQ;
-#pragma unroll
-          for (int j = 0; j < 4; j++) acc[lp][lq][j] = fmaf(t[(i - 1) & 1][j], s8[lq], acc[lp][lq][j]);
-        }
-        if constexpr (p < TP - 2) {
-          // A of p + 1, and in p = TP - 3 also that of the last p
-          constexpr int R = p == TP - 3 ? 4 : 2, r0 = q * R / TQ, r1 = (q + 1) * R / TQ;
-          static_for<r1 - r0>([&](auto r) __attribute__((always_inline)) {
-            constexpr int k = r0 + r, pp = p + 1 + k / 2;
-            fa.read(ta, pp, k % 2, a8[buf(pp)][k % 2]);
-          });
-        } else {
-          constexpr int TICKS = 2 * TQ, k = (p - (TP - 2)) * TQ + q;
-          if constexpr (p == TP - 1) {
-            if constexpr (q < 2) fa.read(na, 0, q, a8[0][q]);  // (free since p = TP - 2 ended)
-            fb.read(nb, q, 0, b8[q][0]);
-            fb.read(nb, q, 1, b8[q][1]);
-          }
-          constexpr int j0 = k * LOADS / TICKS, j1 = (k + 1) * LOADS / TICKS;
-          static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(slot, j0 + j); });
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    });
-    constexpr int L = TP * TQ - 1;
-#pragma unroll
-    for (int j = 0; j < 4; j++) acc[TP - 1][TQ - 1][j] = fmaf(t[L & 1][j], s8[TQ - 1], acc[TP - 1][TQ - 1][j]);
-    read_scales(next, s8);
-    close();
-    warm();
-    slot = next;
-  };
-
   auto stage_fp8 = [&]() __attribute__((always_inline)) {
     wait_loads();
     barrier_only();
@@ -553,22 +486,14 @@ __global__ __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && NS * (BP + BQ) * KB >
     stored = P % (OUT_BF16 ? 8 : 4) == 0;
   };
 
-  constexpr int AHEAD = DT == kFp8Exact ? NS - 1 : NS;  // stages loaded before the first one multiplies
+  constexpr int AHEAD = FP8 ? NS - 1 : NS;  // stages loaded before the first one multiplies
 #pragma unroll
   for (int s = 0; s < AHEAD; s++) issue(s);
-  if constexpr (DT != kFp8Exact) {
+  if constexpr (!FP8) {
     wait_vm<(NS - 1) * OPS + OPS - LOADS>();
     barrier_only();
-    if constexpr (DT == kFp8Native) {
 #pragma unroll
-      for (int i = 0; i < 2 * TQ; i++) fb.read(lds + T::ATile::kBytes, i / 2, i % 2, b8[i / 2][i % 2]);
-#pragma unroll
-      for (int i = 0; i < 2; i++) fa.read(lds, 0, i, a8[0][i]);
-      read_scales(0, s8);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NR; i++) read(0, 0, 0, i);
-    }
+    for (int i = 0; i < NR; i++) read(0, 0, 0, i);
   }
   for (;;) {
 #pragma unroll
@@ -576,10 +501,8 @@ __global__ __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && NS * (BP + BQ) * KB >
 #pragma unroll
       for (int q = 0; q < TQ; q++) acc[p][q] = zero4();
     const int n_stages = (o.len + PER - 1) / PER;
-    if constexpr (DT == kFp8Exact) {
+    if constexpr (FP8) {
       for (int s = 0; s < n_stages; s++) stage_fp8();
-    } else if constexpr (DT == kFp8Native) {
-      for (int s = 0; s < n_stages; s++) stage_native();
     } else {
       for (int s = 0; s < n_stages; s++) stage();
     }
@@ -618,8 +541,6 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   };
   if (out_bf16)
     launch(std::integral_constant<int, kOutBf16>{});
-  else if constexpr (DT == kFp8Native)
-    return hipErrorInvalidValue;
   else if constexpr (PROD == kWgrad)
     a.accumulate ? launch(std::integral_constant<int, kOutAdd>{}) : launch(std::integral_constant<int, kOutF32>{});
   else
