@@ -6,13 +6,16 @@ int32 [E]; ``AlignOut.offsets`` and ``AlignOut.counts`` are in this form.  ``exp
 many rows the experts hold together (T * k; None: all rows).  Rows of no expert are left as they are in
 ``out``, and undefined in an output allocated here.
 
-All tensors of a call are on one device, whose current stream the call uses unless ``stream`` is given.
+All tensors of a call are on one device, whose current stream the call uses unless ``stream`` is given.  Then the
+caller sees to it that ``stream`` comes after the work that makes the operands, and outputs allocated here belong to
+``stream``, as if the call were made under ``torch.cuda.stream(stream)``.
 """
 from __future__ import annotations
 
 import torch
 
 from ._lib import MOE_LAYOUT_ROWS, MOE_OUT_BF16, MOE_OUT_F32, check, lib
+from ._streams import allocating_on
 
 _OUT = {torch.float32: MOE_OUT_F32, torch.bfloat16: MOE_OUT_BF16}
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -41,9 +44,10 @@ def _ranges(offsets: torch.Tensor, counts: torch.Tensor | None, E: int, device):
     return offsets.data_ptr(), _operand(counts, (torch.int32,), (E,), device, "counts") if counts is not None else None
 
 
-def _output(out, out_dtype, shape, device):
+def _output(out, out_dtype, shape, device, stream=None):
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=device)
+        with allocating_on(stream, device):
+            out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
     if out.dtype not in _OUT:
@@ -76,7 +80,7 @@ def _grouped(name, a, b, offsets, counts, expected_rows, E, N, K, out, out_dtype
     """a: the row matrix that the call is named by; b: the other operand, both checked."""
     dev = a.device
     off, cnt = _ranges(offsets, counts, E, dev)
-    out, po, code = _output(out, out_dtype, shape, dev)
+    out, po, code = _output(out, out_dtype, shape, dev, stream)
     M = a.shape[0]
     _call(name, dev, stream, a.data_ptr(), b.data_ptr(), off, cnt, E, M, M if expected_rows is None else expected_rows,
           N, K, po, code, *more)
@@ -129,8 +133,9 @@ def moe_quantize_blocks(x: torch.Tensor, q: torch.Tensor | None = None, scale: t
     """bf16 rows [M, K] to e4m3 codes [M, K] and f32 scales [ceil(K / 128), M], one per row and 128 columns."""
     M, K = _matrix(x, 2, "x")
     dev, KB = x.device, (K + 127) // 128
-    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-    scale = torch.empty((KB, M), dtype=torch.float32, device=dev) if scale is None else scale
+    with allocating_on(stream, dev):
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
+        scale = torch.empty((KB, M), dtype=torch.float32, device=dev) if scale is None else scale
     _call("moe_quantize_blocks", dev, stream, _operand(x, _BF16, (M, K), dev, "x"), M, K,
           _operand(q, _CODES, (M, K), dev, "q"), _operand(scale, (torch.float32,), (KB, M), dev, "scale"))
     return q, scale
@@ -145,7 +150,7 @@ def moe_block_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch
     N, _ = _matrix(wq, 2, "wq")
     dev, NB, KB = xq.device, (N + 127) // 128, (K + 127) // 128
     f32 = (torch.float32,)
-    out, po, code = _output(out, out_dtype, (M, N), dev)
+    out, po, code = _output(out, out_dtype, (M, N), dev, stream)
     _call("moe_block_mm", dev, stream, _operand(xq, _CODES, (M, K), dev, "xq"), _operand(xs, f32, (KB, M), dev, "xs"),
           _operand(wq, _CODES, (N, K), dev, "wq"), _operand(ws, f32, (NB, KB), dev, "ws"), layout, M, N, K, po, code)
     return out
@@ -161,7 +166,7 @@ def moe_grouped_block_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, w
     dev, NB, KB = xq.device, (N + 127) // 128, (K + 127) // 128
     f32 = (torch.float32,)
     off, cnt = _ranges(offsets, counts, E, dev)
-    out, po, code = _output(out, out_dtype, (M, N), dev)
+    out, po, code = _output(out, out_dtype, (M, N), dev, stream)
     _call("moe_grouped_block_mm", dev, stream, _operand(xq, _CODES, (M, K), dev, "xq"),
           _operand(xs, f32, (KB, M), dev, "xs"), _operand(wq, _CODES, (E, N, K), dev, "wq"),
           _operand(ws, f32, (E, NB, KB), dev, "ws"), layout, off, cnt, E, M, M if expected_rows is None else expected_rows,

@@ -1,0 +1,73 @@
+"""Calls with ``stream=S`` and no output: what the binding allocates belongs to S.
+
+Each call is made twice.  First with work queued on the current stream that will still write a block freed there (a
+sleep, then a fill): an output that took that block would be overwritten by the fill.  Then with S asleep, so that the
+call's kernels run late: memory that the call took from the current stream's pool and gave back would by then belong to
+a new tensor there, and the kernels would write into it.  The queued fills and kernels are ordinary work inside live
+allocations of the process; only values can come out wrong.
+"""
+import pytest
+import torch
+
+import quantized_moe_expert_topk_amd as qm
+from tests.test_gpu_grouped import fp8_rows, fp8_weights, gen, ints, ranges
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+SLEEP = 100_000_000  # cycles: some tens of milliseconds at least
+
+
+def grouped_inputs():
+    N, K = 1024, 512
+    off, cnt, M = ranges([300, 0, 257, 467])
+    g = gen(1)
+    x, w, dy = ints(g, M, K), ints(g, 4, N, K), ints(g, M, N)
+    xq, xs = fp8_rows(g, M, K, "ints")
+    wq, ws = fp8_weights(g, 4, N, K, "ints")
+    return {
+        "moe_grouped_mm": lambda s: [qm.moe_grouped_mm(x, w, off, cnt, stream=s)],
+        "moe_grouped_mm_dgrad": lambda s: [qm.moe_grouped_mm_dgrad(dy, w, off, cnt, stream=s)],
+        "moe_grouped_mm_wgrad": lambda s: [qm.moe_grouped_mm_wgrad(dy, x, off, cnt, stream=s)],
+        "moe_quantize_blocks": lambda s: list(qm.moe_quantize_blocks(x, stream=s)),
+        "moe_block_mm": lambda s: [qm.moe_block_mm(xq, xs, wq[0], ws[0], stream=s)],
+        "moe_grouped_block_mm": lambda s: [qm.moe_grouped_block_mm(xq, xs, wq, ws, off, cnt, stream=s)],
+    }
+
+
+def bits(ts):
+    return [t.contiguous().view(torch.uint8) for t in ts]
+
+
+def check_on_another_stream(call, raw, extra=()):
+    """`extra`: sizes in bytes of temporary memory that the call takes besides its outputs."""
+    S = torch.cuda.Stream()
+    handle = S.cuda_stream if raw else S
+    want = [t.clone() for t in bits(call(None))]
+    sizes = [t.numel() for t in want] + list(extra)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+    torch.cuda._sleep(SLEEP)
+    for t in old:
+        t.fill_(0xFF)
+    del old, t
+    got = call(handle)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(bits(got), want)), "written by the current stream's earlier work"
+    del got
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(S):
+        torch.cuda._sleep(SLEEP)
+    got = call(handle)
+    del got
+    new = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x55) for n in sizes]
+    torch.cuda.synchronize()
+    assert all(bool((t == 0x55).all()) for t in new), "the call wrote into memory given to other work"
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("name", ["moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad",
+                                       "moe_quantize_blocks", "moe_block_mm", "moe_grouped_block_mm"])
+def test_outputs_belong_to_the_stream_of_the_call(name, raw):
+    check_on_another_stream(grouped_inputs()[name], raw)
