@@ -1,6 +1,7 @@
 """Python binding of the C ABI in ``include/qmoe.h``: the same entry points, taking torch
 device tensors.  Argument marshalling only; every step runs in the gfx950 kernels of
-``libqmoe.so``.  Output tensors are allocated with torch when the caller passes none.
+``libqmoe.so``.  Output tensors and workspaces are allocated with torch when the caller passes none, on ``stream``
+where one is given.
 """
 from __future__ import annotations
 
@@ -13,7 +14,7 @@ import torch
 from . import _lib
 from ._lib import (MOE_FMT, MOE_LAYOUT_ROWS, MOE_LAYOUT_TILE16, MOE_OUT_BF16, MOE_OUT_F32, MoeAlignOutStruct,
                    MoeBankStruct, check, lib)
-
+from ._streams import allocating_on
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -100,13 +101,14 @@ def moe_pack_bank(bank: DeviceBank, stream=None) -> DeviceBank:
     def like(t, rows, cols):  # new storage, [E, rows, cols] of t's dtype
         return torch.empty((E, rows, cols), dtype=t.dtype, device=t.device)
 
-    if bank.fmt in ("nvfp4", "mxfp4", "q4_0"):  # codes and scales are reordered
-        sdiv = 16 if bank.fmt == "nvfp4" else 32  # scale elements per row: K / sdiv
-        gu, dn = like(bank.gate_up, 2 * I, H // 2), like(bank.down, H, I // 2)
-        gus, dns = like(bank.gate_up_scale, 2 * I, H // sdiv), like(bank.down_scale, H, I // sdiv)
-    else:  # codes only
-        gu, dn = torch.empty_like(bank.gate_up), torch.empty_like(bank.down)
-        gus, dns = bank.gate_up_scale, bank.down_scale
+    with allocating_on(stream, bank.gate_up.device):
+        if bank.fmt in ("nvfp4", "mxfp4", "q4_0"):  # codes and scales are reordered
+            sdiv = 16 if bank.fmt == "nvfp4" else 32  # scale elements per row: K / sdiv
+            gu, dn = like(bank.gate_up, 2 * I, H // 2), like(bank.down, H, I // 2)
+            gus, dns = like(bank.gate_up_scale, 2 * I, H // sdiv), like(bank.down_scale, H, I // sdiv)
+        else:  # codes only
+            gu, dn = torch.empty_like(bank.gate_up), torch.empty_like(bank.down)
+            gus, dns = bank.gate_up_scale, bank.down_scale
     dst = DeviceBank(bank.fmt, E, H, I, gu, gus, dn, dns, bank.gate_up_global, bank.down_global, MOE_LAYOUT_TILE16)
     src_s, dst_s = bank.struct(), dst.struct()
     check("moe_pack_bank", lib().moe_pack_bank(ctypes.byref(src_s), ctypes.byref(dst_s), _stream(stream)))
@@ -125,9 +127,10 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | None
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
-    logits = torch.empty((T, E), dtype=torch.float32, device=dev) if logits is None else logits
-    topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    with allocating_on(stream, dev):
+        logits = torch.empty((T, E), dtype=torch.float32, device=dev) if logits is None else logits
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
     _need(x, torch.bfloat16, (T, H), "x")
     _need(w_router, torch.bfloat16, (E, H), "w_router")
     if bias is not None:
@@ -137,7 +140,8 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | None
     _need(topk_w, torch.float32, (T, k), "topk_w")
     need = moe_route_workspace_bytes(T, H, E)
     if workspace is None and need:
-        workspace = _workspace(need, dev)
+        with allocating_on(stream, dev):
+            workspace = _workspace(need, dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check("moe_route", lib().moe_route(_ptr(x), T, H, _ptr(w_router), E, _ptr(bias), k, int(renormalize),
                                        _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace), ws_bytes,
@@ -149,8 +153,9 @@ def moe_route_from_logits(logits: torch.Tensor, k: int, bias: torch.Tensor | Non
                           topk_ids=None, topk_w=None, stream=None):
     T, E = logits.shape
     dev = logits.device
-    topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    with allocating_on(stream, dev):
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
     _need(logits, torch.float32, (T, E), "logits")
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
@@ -181,10 +186,11 @@ def moe_align(topk_ids: torch.Tensor, E: int, block_m: int, out: AlignOut | None
               workspace: torch.Tensor | None = None, stream=None) -> AlignOut:
     T, k = topk_ids.shape
     _need(topk_ids, torch.int32, (T, k), "topk_ids")
-    out = alloc_align(T, k, E, block_m, topk_ids.device) if out is None else out
     need = moe_align_workspace_bytes(T, k, E)
-    if workspace is None and need:
-        workspace = _workspace(need, topk_ids.device)
+    with allocating_on(stream, topk_ids.device):
+        out = alloc_align(T, k, E, block_m, topk_ids.device) if out is None else out
+        if workspace is None and need:
+            workspace = _workspace(need, topk_ids.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = out.struct()
     check("moe_align", lib().moe_align(_ptr(topk_ids), T, k, E, ctypes.byref(st), _ptr(workspace), ws_bytes,
@@ -204,9 +210,10 @@ def moe_route_align(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor 
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
-    logits = torch.empty((T, E), dtype=torch.float32, device=dev) if logits is None else logits
-    topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    with allocating_on(stream, dev):
+        logits = torch.empty((T, E), dtype=torch.float32, device=dev) if logits is None else logits
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
     _need(x, torch.bfloat16, (T, H), "x")
     _need(w_router, torch.bfloat16, (E, H), "w_router")
     if bias is not None:
@@ -214,10 +221,12 @@ def moe_route_align(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor 
     _need(logits, torch.float32, (T, E), "logits")
     _need(topk_ids, torch.int32, (T, k), "topk_ids")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    out = alloc_align(T, k, E, block_m, dev) if out is None else out
+    with allocating_on(stream, dev):
+        out = alloc_align(T, k, E, block_m, dev) if out is None else out
     need = moe_route_align_workspace_bytes(T, H, E, k)
     if workspace is None and need:
-        workspace = _workspace(need, dev)
+        with allocating_on(stream, dev):
+            workspace = _workspace(need, dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = out.struct()
     check("moe_route_align", lib().moe_route_align(_ptr(x), T, H, _ptr(w_router), E, _ptr(bias), k, int(renormalize),
@@ -236,10 +245,11 @@ def moe_workspace_bytes(routed: DeviceBank, shared: DeviceBank | None, T: int, k
                                          block_m, slice_lo, slice_hi))
 
 
-def _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, device):
+def _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, device, stream):
     need = moe_workspace_bytes(routed, shared, T, k, align.block_m, slice_lo, slice_hi)
     if workspace is None:
-        workspace = _workspace(need, device)
+        with allocating_on(stream, device):
+            workspace = _workspace(need, device)
     rs, ss, al = routed.struct(), (shared.struct() if shared is not None else None), align.struct()
     return workspace, rs, ss, al
 
@@ -252,9 +262,10 @@ def moe_expert_forward(routed: DeviceBank, shared: DeviceBank | None, x: torch.T
     k = topk_w.shape[1]
     _need(x, torch.bfloat16, (T, H), "x")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    out = torch.empty((T, H), dtype=out_dtype, device=x.device) if out is None else out
+    with allocating_on(stream, x.device):
+        out = torch.empty((T, H), dtype=out_dtype, device=x.device) if out is None else out
     _need(out, out_dtype, (T, H), "out")
-    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, x.device)
+    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, x.device, stream)
     code = MOE_OUT_BF16 if out_dtype == torch.bfloat16 else MOE_OUT_F32
     check("moe_expert_forward", lib().moe_expert_forward(
         ctypes.byref(rs), ctypes.byref(ss) if ss is not None else None, _ptr(x), T, k, _ptr(topk_w),
@@ -283,7 +294,7 @@ def moe_expert_gate_up(routed: DeviceBank, shared: DeviceBank | None, x: torch.T
                        slice_lo: int, slice_hi: int, workspace: torch.Tensor, stream=None) -> None:
     T, H = x.shape
     _need(x, torch.bfloat16, (T, H), "x")
-    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, x.device)
+    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, x.device, stream)
     check("moe_expert_gate_up", lib().moe_expert_gate_up(
         ctypes.byref(rs), ctypes.byref(ss) if ss is not None else None, _ptr(x), T, k, ctypes.byref(al),
         slice_lo, slice_hi, _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -293,7 +304,7 @@ def moe_expert_down(routed: DeviceBank, shared: DeviceBank | None, topk_w: torch
                     slice_lo: int, slice_hi: int, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     T, k = topk_w.shape
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, out.device)
+    workspace, rs, ss, al = _fwd_common(routed, shared, T, k, align, slice_lo, slice_hi, workspace, out.device, stream)
     code = MOE_OUT_BF16 if out.dtype == torch.bfloat16 else MOE_OUT_F32
     check("moe_expert_down", lib().moe_expert_down(
         ctypes.byref(rs), ctypes.byref(ss) if ss is not None else None, T, k, _ptr(topk_w), ctypes.byref(al),

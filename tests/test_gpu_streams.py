@@ -1,4 +1,4 @@
-"""Calls with ``stream=S`` and no output: what the binding allocates belongs to S.
+"""Calls with ``stream=S`` and no output or workspace: what the binding allocates belongs to S.
 
 Each call is made twice.  First with work queued on the current stream that will still write a block freed there (a
 sleep, then a fill): an output that took that block would be overwritten by the fill.  Then with S asleep, so that the
@@ -71,3 +71,43 @@ def check_on_another_stream(call, raw, extra=()):
                                        "moe_quantize_blocks", "moe_block_mm", "moe_grouped_block_mm"])
 def test_outputs_belong_to_the_stream_of_the_call(name, raw):
     check_on_another_stream(grouped_inputs()[name], raw)
+
+
+def layer_inputs():
+    from synth import synth as S
+    from tests.gpu_util import bf16_dev, device_bank
+    T = 75
+    cfg = S.LayerConfig(91, "small layer", "bf16", 256, 8, 2, 256, False, (T,), ((0, 256),))
+    inp = S.layer_inputs(cfg, T)
+    x, router, bank, rows = bf16_dev(inp.x), bf16_dev(inp.router), device_bank(inp.routed), device_bank(inp.routed, packed=False)
+    logits, ids, wts, al = qm.moe_route_align(x, router, None, cfg.k, 16)
+
+    def aligned(a):
+        """The parts of an alignment that are written whatever the routing."""
+        return [a.counts, a.offsets, a.total_padded]
+
+    def route_align(s):
+        *r, a = qm.moe_route_align(x, router, None, cfg.k, 16, stream=s)
+        return [*r, *aligned(a)]
+
+    def packed(s):
+        b = qm.moe_pack_bank(rows, stream=s)
+        return [b.gate_up, b.down]
+
+    return {
+        "moe_pack_bank": (packed, 0),
+        "moe_route": (lambda s: list(qm.moe_route(x, router, None, cfg.k, stream=s)),
+                      qm.moe_route_workspace_bytes(T, cfg.H, cfg.E)),
+        "moe_route_from_logits": (lambda s: list(qm.moe_route_from_logits(logits, cfg.k, stream=s)), 0),
+        "moe_align": (lambda s: aligned(qm.moe_align(ids, cfg.E, 16, stream=s)), qm.moe_align_workspace_bytes(T, cfg.k, cfg.E)),
+        "moe_route_align": (route_align, qm.moe_route_align_workspace_bytes(T, cfg.H, cfg.E, cfg.k)),
+        "moe_expert_forward": (lambda s: [qm.moe_expert_forward(bank, None, x, wts, al, 0, cfg.I, stream=s)],
+                               qm.moe_workspace_bytes(bank, None, T, cfg.k, 16, 0, cfg.I)),
+    }
+
+
+@pytest.mark.parametrize("name", ["moe_pack_bank", "moe_route", "moe_route_from_logits", "moe_align", "moe_route_align",
+                                  "moe_expert_forward"])
+def test_memory_of_the_layer_calls_belongs_to_their_stream(name):
+    call, workspace = layer_inputs()[name]
+    check_on_another_stream(call, False, [workspace] if workspace else [])
