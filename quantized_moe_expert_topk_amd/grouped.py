@@ -133,9 +133,10 @@ def moe_quantize_blocks(x: torch.Tensor, q: torch.Tensor | None = None, scale: t
     """bf16 rows [M, K] to e4m3 codes [M, K] and f32 scales [ceil(K / 128), M], one per row and 128 columns."""
     M, K = _matrix(x, 2, "x")
     dev, KB = x.device, (K + 127) // 128
-    with allocating_on(stream, dev):
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-        scale = torch.empty((KB, M), dtype=torch.float32, device=dev) if scale is None else scale
+    if q is None or scale is None:
+        with allocating_on(stream, dev):
+            q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
+            scale = torch.empty((KB, M), dtype=torch.float32, device=dev) if scale is None else scale
     _call("moe_quantize_blocks", dev, stream, _operand(x, _BF16, (M, K), dev, "x"), M, K,
           _operand(q, _CODES, (M, K), dev, "q"), _operand(scale, (torch.float32,), (KB, M), dev, "scale"))
     return q, scale
