@@ -9,6 +9,10 @@ many rows the experts hold together (T * k; None: all rows).  Rows of no expert 
 All tensors of a call are on one device, whose current stream the call uses unless ``stream`` is given.  Then the
 caller sees to it that ``stream`` comes after the work that makes the operands, and outputs allocated here belong to
 ``stream``, as if the call were made under ``torch.cuda.stream(stream)``.
+
+Nothing is recorded for autograd: tensors that require gradients are refused while gradients are recorded, as a result
+without a history would be a silent loss.  Call under ``torch.no_grad()``, or from ``torch.autograd.Function``'s methods
+(where nothing is recorded) with :func:`moe_grouped_mm_dgrad` and :func:`moe_grouped_mm_wgrad` as the backward.
 """
 from __future__ import annotations
 
@@ -22,6 +26,8 @@ _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _operand(t: torch.Tensor, dtypes, shape, device, name: str) -> int:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires gradients, which this call does not record; call it under torch.no_grad()")
     if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name}: expected contiguous {' or '.join(map(str, dtypes))} {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
