@@ -3,6 +3,8 @@
 //   scale[b, r] = max |x[r, k]| over the block / 448,   q[r, k] = e4m3(x[r, k] / scale[b, r])
 //
 // A workgroup owns 32 rows x 4 blocks; 16 lanes hold a block, 8 values each.
+#include <algorithm>
+
 #include "grouped_dev.h"
 
 namespace qmoe {
@@ -35,10 +37,11 @@ __device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale) {
+__global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int first, int M, int K, uint8_t *q,
+                                                         float *scale) {
   __shared__ float sc[QBLOCKS][QROWS];
   const int tid = threadIdx.x, blk = (tid >> 4) & 3, r4 = tid >> 6;  // a wave: one row, 4 blocks
-  const size_t row0 = (size_t)blockIdx.x * QROWS;
+  const size_t row0 = (size_t)first + (size_t)blockIdx.x * QROWS;
   const int kb0 = blockIdx.y * QBLOCKS, k = kb0 * 128 + (tid & 63) * 8;
   constexpr int NP = QROWS / 4;
   frag8 v[NP];
@@ -93,9 +96,15 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int 
 }
 
 hipError_t launch_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale, hipStream_t s) {
-  const dim3 grid((M + QROWS - 1) / QROWS, ((K + 127) / 128 + QBLOCKS - 1) / QBLOCKS);
-  k_quantize_blocks<<<grid, 256, 0, s>>>(x, M, K, q, scale);
-  return hipGetLastError();
+  // A launch has fewer than 2^32 threads along x, 2^29 rows: more rows take several.
+  constexpr int ROWS = 1 << 28;
+  for (long long first = 0; first < M; first += ROWS) {
+    const int rows = (int)std::min<long long>(ROWS, M - first);
+    const dim3 grid((rows + QROWS - 1) / QROWS, ((K + 127) / 128 + QBLOCKS - 1) / QBLOCKS);
+    k_quantize_blocks<<<grid, 256, 0, s>>>(x, (int)first, M, K, q, scale);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace qmoe
