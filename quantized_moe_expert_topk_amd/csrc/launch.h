@@ -149,8 +149,7 @@ struct ProductArgs {
 
 // rows: about how many rows all groups hold together; it picks the kernel, never the result's meaning.
 hipError_t launch_grouped_mm(int prod, const ProductArgs &a, int rows, bool out_bf16, hipStream_t s);
-// Both forward products where experts have few rows.
-bool few_rows_faster(const ProductArgs &a, int rows, int elem, double ring_us);
+// Both forward products where experts have few rows (tiles.h).
 hipError_t launch_few_rows(ProductArgs a, bool fp8, bool out_bf16, hipStream_t s);
 hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStream_t s);
 hipError_t launch_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale, hipStream_t s);

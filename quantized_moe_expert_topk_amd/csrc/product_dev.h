@@ -4,10 +4,12 @@
 #pragma once
 
 #include <algorithm>
+#include <iterator>
 #include <type_traits>
 #include <utility>
 
 #include "grouped_dev.h"
+#include "tiles.h"
 
 namespace qmoe {
 
@@ -546,6 +548,19 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   else
     launch(std::integral_constant<int, kOutF32>{});
   return hipGetLastError();
+}
+
+// The product with tile t of TILES.
+template <int PROD, int DT, const auto &TILES, size_t... I>
+hipError_t run_tile_of(int t, const ProductArgs &a, bool out_bf16, hipStream_t s, std::index_sequence<I...>) {
+  hipError_t e = hipErrorInvalidValue;
+  (void)((t == (int)I && (e = run_product<PROD, DT, TILES[I].bp, TILES[I].bq, TILES[I].wp, TILES[I].wq,
+                                          TILES[I].stages, TILES[I].nt>(a, out_bf16, s), true)) || ...);
+  return e;
+}
+template <int PROD, int DT, const auto &TILES>
+hipError_t run_tile(int t, const ProductArgs &a, bool out_bf16, hipStream_t s) {
+  return run_tile_of<PROD, DT, TILES>(t, a, out_bf16, s, std::make_index_sequence<std::size(TILES)>{});
 }
 
 }  // namespace qmoe

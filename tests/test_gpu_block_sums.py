@@ -22,7 +22,7 @@ DEV, FP8 = "cuda", torch.float8_e4m3fn
 BOTH = (torch.float32, torch.bfloat16)
 
 # (M, N, K): one row, few rows, and each tile that the launcher picks by rows and outputs
-DENSE = [(1, 1024, 2048), (5, 4096, 128), (16, 8192, 128), (40, 4096, 128), (64, 130, 2048), (100, 384, 1040), (256, 4096, 512),
+DENSE = [(1, 1024, 2048), (5, 4096, 128), (16, 8192, 128), (40, 4096, 128), (64, 130, 2048), (100, 384, 1040), (256, 4096, 512), (500, 4096, 272),
          (600, 1320, 1040), (1000, 2050, 272), (2100, 4096, 272), (4100, 4100, 400)]
 GROUPS = {
     "tiny": [3, 0, 1, 2],
