@@ -32,14 +32,8 @@ constexpr int kBf16 = 0, kFp8 = 1;
 
 constexpr int kOutF32 = 0, kOutBf16 = 1, kOutAdd = 2;  // kOutAdd: add to fp32
 
-// Cache policy of the stores of large outputs: non-temporal, written through to memory.  Nothing here reads them
-// again, and lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows,
-// N 1024, K 2048: 349 us with the default policy, 278 with the non-temporal hint, 246 with both).  Outputs that L2
-// can hold keep the default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.  And rows that
-// end inside a 128-byte line do: their part lines went to memory one by one (wgrad of 60 experts, 1912 x 728: 159 us
-// written through, 33 not).
+// Cache policy of the stores where stores_go_through() (tiles.h) says so: non-temporal, written through to memory.
 constexpr int kWriteThrough = 2 | 16;
-constexpr double kThroughBytes = 16e6;
 
 template <int PROD, int BP, int BQ, int WP, int WQ>
 struct ProductTypes {
@@ -528,7 +522,7 @@ hipError_t run_product(ProductArgs a, bool out_bf16, hipStream_t s) {
   }
   a.q_run = (int)std::max(1LL, std::min(4LL, q));
   const double out_bytes = (double)(PROD == kWgrad ? (long long)a.g.E * a.N : a.g.M) * P * (out_bf16 ? 2 : 4);
-  a.write_through = out_bytes > kThroughBytes && (long long)P * (out_bf16 ? 2 : 4) % 128 == 0;
+  a.write_through = stores_go_through(a.out, out_bytes, (long long)P * (out_bf16 ? 2 : 4));
   const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
   if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
   constexpr int LDS = NS * ((BP + BQ) * KB + (DT != kBf16 ? 4 * (BQ > 64 ? BQ : 64) + 256 : 0)) + kMaxExperts * 4 + 512;

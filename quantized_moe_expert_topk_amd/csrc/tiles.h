@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstdint>
 
 #include "launch.h"
 
@@ -118,6 +119,16 @@ inline int choose_block(const ProductArgs &a, int rows) {
   if (mean <= 16 || tiles(32) <= 256) return 0;
   if (mean <= 64 || tiles(64) <= 256) return 1;
   return tiles(128) <= 256 ? 2 : 3;
+}
+
+// Whether k_product's outputs are stored non-temporal and written through to memory.  Nothing here reads them again, and
+// lines that stay dirty in L2 hold up the loads and stores behind them (wgrad of 256 experts of 128 rows, N 1024, K 2048:
+// 349 us with the default policy, 278 with the non-temporal hint, 246 with both).  Outputs that L2 can hold keep the
+// default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.  And rows that begin or end inside
+// a 128-byte line do: their part lines went to memory one by one (wgrad of 60 experts, 1912 x 728: 159 us written
+// through, 33 not; of 256 experts of 128 rows with the output 16 bytes off a line: 1067, 340 not).
+inline bool stores_go_through(const void *out, double bytes, long long pitch) {
+  return bytes > 16e6 && pitch % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
 }
 
 }  // namespace qmoe

@@ -31,4 +31,8 @@ int tile_outputs(int prod, int t) {
   const Tile *const tiles[] = {kForwardTiles, kDgradTiles, kWgradTiles, kFp8Tiles};
   return tiles[prod][t].bp * 1000 + tiles[prod][t].bq;
 }
+
+int through(uint64_t out, double bytes, long long pitch) {
+  return stores_go_through(reinterpret_cast<const void *>(out), bytes, pitch);
+}
 }

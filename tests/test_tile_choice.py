@@ -81,3 +81,14 @@ def test_choices_exist_over_the_whole_range(tiles):
                 for grouped in ((1,) if prod != BLOCK else (0, 1)):
                     t = tiles.choose(prod, grouped, E if grouped else 1, M, rows, N, K)
                     assert (-1 if prod in (FORWARD, BLOCK) else 0) <= t < tiles.tile_count(prod)
+
+
+def test_only_whole_lines_are_written_through(tiles):
+    """Large outputs whose rows begin and end with a 128-byte line; a view 16 bytes further does neither."""
+    through = lambda out, nbytes, pitch: tiles.through(ctypes.c_uint64(out), ctypes.c_double(nbytes), ctypes.c_longlong(pitch))
+    assert through(1 << 40, 1e8, 4096) == 1
+    assert through((1 << 40) + 128, 1e8, 128) == 1
+    for off in (16, 32, 64, 112):
+        assert through((1 << 40) + off, 1e8, 4096) == 0
+    assert through(1 << 40, 1e8, 4096 + 64) == 0
+    assert through(1 << 40, 1e6, 4096) == 0
