@@ -66,10 +66,11 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const uint16_t *x, int 
       f[2 * j] = __uint_as_float(v[i].u[j] << 16);
       f[2 * j + 1] = __uint_as_float(v[i].u[j] & 0xFFFF0000u);
     }
-    // x / d rounded to nearest, three operations an element: with r the rounded 1 / d and t = x r within one
-    // unit of the quotient, x - t d is exact in one fma and t + r (x - t d) rounds to the quotient (Markstein).
-    // Exact means no underflow: a quotient that e4m3 does not round to 0 is at least 2^-10, so d >= 2^-60 is
-    // far enough.  Blocks of other magnitudes (and NaN) divide.
+    // x / d rounded to nearest, three operations an element (Markstein): with r the rounded 1 / d and t = x r, within
+    // 1.4 units of the quotient, t + r (x - t d) rounds to the quotient.  For all 128 x 128 mantissas of x and of the
+    // block's maximum, which is every case there is where nothing underflows: tests/test_quantize_division.py goes
+    // through them.  A quotient that e4m3 does not round to 0 is at least 2^-10, so d >= 2^-60 is far enough.  Blocks of
+    // other magnitudes (and NaN) divide.
     if (d >= 0x1p-60f && d <= 0x1p60f) {
       const float r = 1.f / d;
 #pragma unroll
