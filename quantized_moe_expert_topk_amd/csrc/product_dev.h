@@ -51,10 +51,11 @@ struct OutTile {
   int row0, len;        // wgrad: the expert's first row; len: the contraction in 16-byte units (forward) or rows
 };
 
-// The tiled product.  What bounds it: large groups run at the card's power limit (8 experts of 2048 rows, N and K
-// 4096: about 1.28 PFLOP/s in each of the three products at 2.0 GHz, the matrix cores busy 97% of a stage's
-// cycles when loads are left out; a library product of the same size reaches 1.2 to 1.56 by layout), small
-// groups by reading the weights (4.0 TB/s at 256 rows an expert, 5.2 at 128, 5.8 at 2).  Choices:
+// The tiled product.  What bounds it: in large groups the stages' loads and LDS reads beside the matrix cores (8 experts
+// of 2048 rows, N and K 4096, bf16 outputs: 1.28, 1.27 and 1.30 PFLOP/s forward, dgrad and wgrad, the matrix cores busy
+// 55% of the launch's cycles and waves waiting for 31% of theirs; 97% of a stage's cycles when loads are left out; a
+// library product of that size reaches 1.56), in wgrad with fp32 outputs also their stores (1.19; 0.90 where they are added to), in small groups
+// reading the weights (4.0 TB/s at 256 rows an expert, 5.2 at 128, 5.8 at 2).  Choices:
 // - 16 x 16 matrix instructions (RowFrag says why), a wave tile of 64 x 64 to 128 x 64: operands from LDS once
 //   per 64 to 128 columns, and two waves a SIMD.
 // - stages of 128 bytes of c: 64-byte pieces of rows took a third longer to load.
@@ -64,7 +65,7 @@ struct OutTile {
 // - NT: the weights are loaded with the non-temporal hint, for experts whose rows fill one row tile: then each
 //   weight tile is read by one workgroup only, and the hint keeps it from pushing out the activations.  256
 //   experts, N 1024, K 2048, forward, us without / with: m = 2 203 / 184, 64 223 / 198, fp8 m = 2 91 / 79.5; but
-//   where several row tiles share the weights 139 / 167 (fp8 8192 x 4096 x 4096).
+//   where several row tiles share the weights 251 / 271 (fp8 8192 x 4096 x 4096, 256 x 128 tiles).
 template <int PROD, int DT, int BP, int BQ, int WP, int WQ, int NS, bool NT, int OUT, bool THROUGH>
 __global__ __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && NS * (BP + BQ) * KB > 81920 ? 1 : 2) void k_product(ProductArgs a) {
   using T = ProductTypes<PROD, BP, BQ, WP, WQ>;
