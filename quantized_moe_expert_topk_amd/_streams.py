@@ -14,5 +14,6 @@ def allocating_on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = int(getattr(stream, "value", stream) or 0)  # (an integer or a ctypes pointer)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)

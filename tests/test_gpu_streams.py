@@ -6,6 +6,8 @@ call's kernels run late: memory that the call took from the current stream's poo
 a new tensor there, and the kernels would write into it.  The queued fills and kernels are ordinary work inside live
 allocations of the process; only values can come out wrong.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -71,6 +73,21 @@ def check_on_another_stream(call, raw, extra=()):
                                        "moe_quantize_blocks", "moe_block_mm", "moe_grouped_block_mm"])
 def test_outputs_belong_to_the_stream_of_the_call(name, raw):
     check_on_another_stream(grouped_inputs()[name], raw)
+
+
+@pytest.mark.parametrize("handle", [0, ctypes.c_void_p(0), ctypes.c_void_p(None)], ids=["0", "pointer 0", "pointer None"])
+def test_a_null_handle_is_the_default_stream(handle):
+    """A raw handle of 0 names the default stream, for the kernels and for what the call allocates."""
+    from quantized_moe_expert_topk_amd._streams import allocating_on
+    call = grouped_inputs()["moe_grouped_mm"]
+    want = call(None)[0].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with allocating_on(handle, torch.device("cuda", torch.cuda.current_device())):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        got = call(handle)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 def layer_inputs():
