@@ -23,6 +23,7 @@ from ._streams import allocating_on
 
 _OUT = {torch.float32: MOE_OUT_F32, torch.bfloat16: MOE_OUT_BF16}
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_INT_MAX = 2 ** 31 - 1  # of the C interface's sizes: ctypes would pass the low bits of a larger number
 
 
 def _operand(t: torch.Tensor, dtypes, shape, device, name: str) -> int:
@@ -37,6 +38,8 @@ def _operand(t: torch.Tensor, dtypes, shape, device, name: str) -> int:
 def _matrix(t: torch.Tensor, dims: int, name: str):
     if t.dim() != dims:
         raise ValueError(f"{name}: expected {dims} dimensions, got shape {tuple(t.shape)}")
+    if not 0 < t.numel() <= _INT_MAX and max(t.shape) > _INT_MAX:  # (numel() is the cheaper one)
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is too large for 32-bit sizes")
     if t.device.type != "cuda":
         raise ValueError(f"{name}: expected a cuda tensor, got one on {t.device}")
     return t.shape
@@ -48,6 +51,20 @@ def _ranges(offsets: torch.Tensor, counts: torch.Tensor | None, E: int, device):
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}] on {device}, got {offsets.dtype} "
                          f"{tuple(offsets.shape)} on {offsets.device}")
     return offsets.data_ptr(), _operand(counts, (torch.int32,), (E,), device, "counts") if counts is not None else None
+
+
+def _rows_hint(expected_rows: int | None, M: int) -> int:
+    if expected_rows is None:
+        return M
+    return expected_rows if 0 <= expected_rows <= _INT_MAX else _INT_MAX if expected_rows > 0 else -1
+
+
+def _experts(offsets: torch.Tensor, counts: torch.Tensor | None) -> int:
+    """How many experts the row ranges are of."""
+    t, rest = (offsets, 1) if counts is None else (counts, 0)
+    if t.dim() != 1 or t.shape[0] <= rest:
+        raise ValueError(f"{'offsets' if rest else 'counts'}: expected the ranges of at least one expert, got shape {tuple(t.shape)}")
+    return t.shape[0] - rest
 
 
 def _output(out, out_dtype, shape, device, stream=None):
@@ -88,8 +105,8 @@ def _grouped(name, a, b, offsets, counts, expected_rows, E, N, K, out, out_dtype
     off, cnt = _ranges(offsets, counts, E, dev)
     out, po, code = _output(out, out_dtype, shape, dev, stream)
     M = a.shape[0]
-    _call(name, dev, stream, a.data_ptr(), b.data_ptr(), off, cnt, E, M, M if expected_rows is None else expected_rows,
-          N, K, po, code, *more)
+    _call(name, dev, stream, a.data_ptr(), b.data_ptr(), off, cnt, E, M,
+          _rows_hint(expected_rows, M), N, K, po, code, *more)
     return out
 
 
@@ -128,7 +145,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     _, K = _matrix(x, 2, "x")
     _operand(dy, _BF16, (M, N), dy.device, "dy")
     _operand(x, _BF16, (M, K), dy.device, "x")
-    E = counts.shape[0] if counts is not None else offsets.shape[0] - 1
+    E = _experts(offsets, counts)
     if accumulate and out is None:
         raise ValueError("accumulate: needs the out to add to")
     return _grouped("moe_grouped_mm_wgrad", dy, x, offsets, counts, expected_rows, E, N, K, out, out_dtype, (E, N, K),
@@ -176,6 +193,6 @@ def moe_grouped_block_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, w
     out, po, code = _output(out, out_dtype, (M, N), dev, stream)
     _call("moe_grouped_block_mm", dev, stream, _operand(xq, _CODES, (M, K), dev, "xq"),
           _operand(xs, f32, (KB, M), dev, "xs"), _operand(wq, _CODES, (E, N, K), dev, "wq"),
-          _operand(ws, f32, (E, NB, KB), dev, "ws"), layout, off, cnt, E, M, M if expected_rows is None else expected_rows,
+          _operand(ws, f32, (E, NB, KB), dev, "ws"), layout, off, cnt, E, M, _rows_hint(expected_rows, M),
           N, K, po, code)
     return out
