@@ -402,7 +402,8 @@ int moe_grouped_mm_wgrad(const void *dy_bf16, const void *x_bf16, const int32_t 
  * per row and 128 consecutive k, weights one per 128 x 128 block (MOE_FMT_FP8_BLOCK128).  The
  * expert layer multiplies such banks with bf16 activations; these take half the activation bytes.
  * The products of codes are exact and their sums fp32, for outputs of either type and whatever
- * kernel the sizes and expected_rows pick; xs * ws is rounded to fp32 first. */
+ * kernel the sizes and expected_rows pick.  xs * ws is rounded to fp32 first, and has to be a
+ * normal fp32 number or 0. */
 
 /* moe_quantize_blocks -- bf16 rows to e4m3 codes and block scales:
  *   scale[b, r] = max |x[r, k]| / 448 over the k of block b = k / 128 (the last one may be short)
