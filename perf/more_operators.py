@@ -378,12 +378,12 @@ def run(state):
                                                    dweights=s["dweights"])
         return drows, dweights, qm.moe_combine_rows(s["dx_rows"], s["slots"], out=s["dx"])
     if s["op"] == "quantize":
-        q, scale = qm.moe_quantize_mxfp4(s["x"], s["slots"], q=s["q"], scale=s["scale"])
-        return qm.moe_dequantize_mxfp4(q, scale, out=s["values"]), scale
+        q, scale = qm.moe_quantize_mx(s["x"], s["slots"], q=s["q"], scale=s["scale"])
+        return qm.moe_dequantize_mx(q, scale, out=s["values"]), scale
     layout = qm.MOE_LAYOUT_TILE16 if s["layout"] == "tile16" else qm.MOE_LAYOUT_ROWS
     if s["op"] == "dense":
-        return qm.moe_mxfp4_mm(s["xq"], s["xs"], s["w"], s["ws"], layout=layout, out=s["y"])
-    return qm.moe_grouped_mxfp4_mm(s["xq"], s["xs"], s["w"], s["ws"], s["offsets"], s["counts"], s["pairs"],
+        return qm.moe_mx_mm(s["xq"], s["xs"], s["w"], s["ws"], layout=layout, out=s["y"])
+    return qm.moe_grouped_mx_mm(s["xq"], s["xs"], s["w"], s["ws"], s["offsets"], s["counts"], s["pairs"],
                                    layout=layout, out=s["y"])
 
 
