@@ -430,6 +430,46 @@ int moe_grouped_block_mm(const void *xq, const float *xs, const void *wq, const 
                          const int32_t *offsets, const int32_t *counts, int E, int M,
                          int expected_rows, int N, int K, void *y, int out_dtype, void *stream);
 
+/* ------------------------------------------------------------------ rows to the experts and back
+ *
+ * What lies around the grouped products: the tokens' rows brought into the experts' row ranges, and the experts'
+ * rows back to the tokens with their routing weights, each with its gradient.  f = t*k + j is token t's j-th pair.
+ *   slots        [T, k] int32 device array: the row of pair f in the row matrices (moe_pair_slots makes it), or a
+ *                value outside [0, M) where the pair has none.  No value makes a call read or write outside its
+ *                matrices.  Rows that two pairs share are read for both; written by both (moe_gather_rows and
+ *                moe_combine_rows_grad) they hold one or the other.
+ *   M            rows of the row matrices.  Rows of no pair are neither read nor written.
+ * Sums are fp32 in a fixed order: results do not vary from call to call.  No call needs a workspace.
+ * Requires T*k < 2^31 - 1024, H a multiple of 8 and at most 2 million, and 16-byte aligned matrices; an output must
+ * not overlap an operand. */
+
+/* moe_pair_slots -- slots[f] = s with sorted_ids[s] = f in the run of expert topk_ids[f], -1 if there is none (an id
+ * outside [0, E), or a pair that is not there).
+ *   sorted_ids [M], offsets and counts as moe_align gives them (counts NULL: the runs end at offsets[e + 1]; offsets
+ *   then has E + 1 entries); every run ascends.  A run is cut to [0, M). */
+int moe_pair_slots(const int32_t *topk_ids, int T, int k, const int32_t *sorted_ids, int M,
+                   const int32_t *offsets, const int32_t *counts, int E, int32_t *slots, void *stream);
+
+/* moe_gather_rows -- rows[slots[f]] = x[f / k]: the bytes of rows of any type.
+ *   x [T, row_bytes], rows [M, row_bytes]; row_bytes a multiple of 16.  Its gradient is moe_combine_rows without
+ *   weights. */
+int moe_gather_rows(const void *x, int T, int k, const int32_t *slots, int row_bytes, int M, void *rows,
+                    void *stream);
+
+/* moe_combine_rows -- out[t] = add[t] + sum_j weights[f] rows[slots[f]], the sum in fp32 in the order of j and then
+ * add (the shared expert's output, say), rounded once.  Every row of out is written.
+ *   rows [M, H] f32 or bf16 (rows_dtype MOE_OUT_*); weights [T, k] f32, or NULL for ones; add [T, H] of out's type,
+ *   or NULL; out [T, H] f32 or bf16.  The weight of a pair without a row is not used. */
+int moe_combine_rows(const void *rows, int rows_dtype, const int32_t *slots, const float *weights,
+                     const void *add, int T, int k, int M, int H, void *out, int out_dtype, void *stream);
+
+/* moe_combine_rows_grad -- the gradients of moe_combine_rows with weights (that of add is dout itself):
+ *   drows[slots[f]] = weights[f] dout[t],   dweights[f] = sum_h rows[slots[f], h] dout[t, h]  (0 without a row).
+ *   dout [T, H] f32 or bf16; rows and drows [M, H] of rows_dtype; dweights [T, k] f32, every element written. */
+int moe_combine_rows_grad(const void *dout, int dout_dtype, const void *rows, int rows_dtype,
+                          const int32_t *slots, const float *weights, int T, int k, int M, int H,
+                          void *drows, float *dweights, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 const char *moe_status_string(int status); /* static text for a status code */

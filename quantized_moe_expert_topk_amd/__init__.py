@@ -13,3 +13,4 @@ from .api import (AlignOut, DeviceBank, MoeLayer, alloc_align, choose_block_m, m
                   moe_route_from_logits, moe_route_workspace_bytes, moe_workspace_bytes)
 from .grouped import (moe_block_mm, moe_grouped_block_mm, moe_grouped_mm, moe_grouped_mm_dgrad,  # noqa: F401
                       moe_grouped_mm_wgrad, moe_quantize_blocks)
+from .rows import moe_combine_rows, moe_combine_rows_grad, moe_gather_rows, moe_pair_slots  # noqa: F401

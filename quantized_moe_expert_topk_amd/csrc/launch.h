@@ -154,4 +154,17 @@ hipError_t launch_few_rows(ProductArgs a, bool fp8, bool out_bf16, hipStream_t s
 hipError_t launch_block_mm(const ProductArgs &a, int rows, bool out_bf16, hipStream_t s);
 hipError_t launch_quantize_blocks(const uint16_t *x, int M, int K, uint8_t *q, float *scale, hipStream_t s);
 
+// ---- token rows to the experts and back (rows.hip)
+
+// g.M: entries of sorted.  The other calls take M rows and slots [T, k]; a slot outside [0, M) is none.
+hipError_t launch_pair_slots(const int32_t *ids, int P, const int32_t *sorted, const Groups &g, int32_t *slots,
+                             hipStream_t s);
+hipError_t launch_gather_rows(const void *x, int T, int k, const int32_t *slots, int M, void *rows, int row_bytes,
+                              hipStream_t s);
+hipError_t launch_combine_rows(const void *rows, bool rows_f32, const int32_t *slots, const float *weights,
+                               const void *add, int T, int k, int M, int H, void *out, bool out_f32, hipStream_t s);
+hipError_t launch_combine_rows_grad(const void *dout, bool dout_f32, const void *rows, bool rows_f32, const int32_t *slots,
+                                    const float *weights, int T, int k, int M, int H, void *drows, float *dweights,
+                                    hipStream_t s);
+
 }  // namespace qmoe
