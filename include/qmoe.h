@@ -470,6 +470,45 @@ int moe_combine_rows_grad(const void *dout, int dout_dtype, const void *rows, in
                           const int32_t *slots, const float *weights, int T, int k, int M, int H,
                           void *drows, float *dweights, void *stream);
 
+/* ------------------------------------------------------------------ MXFP4 products
+ *
+ * Products of e2m1 activations and e2m1 weights (W4A4), both with an e8m0 scale per 32 consecutive k, on the matrix cores'
+ * FP4 instructions: products of codes and scales are exact and their sums fp32.  Codes are packed two a byte, the even k
+ * in the low nibble; the value of a code is e2m1 * 2^(scale - 127), and a scale of 255 makes its block NaN.
+ *   quantised rows  q [M, K / 2] bytes and scale [ceil(K / 128), M, 4] bytes: the four blocks of 128 columns of a row
+ *                   together, and those of neighbouring rows adjacent (what a tile of rows needs at once).  The bytes of
+ *                   blocks past K are written as 0, and read: they must not be 255.
+ * K is a multiple of 32 and at most 2 million; q, x, y and weight codes 16-byte aligned, scales 4-byte aligned; an output
+ * must not overlap an operand. */
+
+/* moe_quantize_mx -- bf16 rows to quantised rows:
+ *   X[t, b] = the least power of two, at least 2^-126, with max |x[t, k]| <= 6 X over the 32 k of block b (nothing
+ *             saturates; a block of zeros has 2^-126)
+ *   q = e2m1(x / X), rounded to nearest, ties to the even code; -0 and what rounds to it keep their sign.
+ * A NaN or infinity in a block makes its scale 255 and its codes 0.
+ *   slots  [T, k] as for moe_gather_rows: token t is quantised once and written to rows slots[t, :]; other rows of q and
+ *          scale stay as they were.  NULL: row t is token t (k is 1 and M is T). */
+int moe_quantize_mx(const void *x_bf16, const int32_t *slots, int T, int k, int M, int K, void *q, void *scale,
+                    void *stream);
+
+/* moe_dequantize_mx -- the values of quantised rows, y [M, K] f32 or bf16 (for gradients through quantised operands, say).
+ * Exact in both types where the value is in the type's range: past it, infinite. */
+int moe_dequantize_mx(const void *q, const void *scale, int M, int K, void *y, int out_dtype, void *stream);
+
+/* y[r, n] = sum_b 2^(xs[r, b] + ws[n, b] - 254) sum_{k in block b} xq[r, k] wq[n, k]
+ *   xq, xs  M quantised rows; y [M, N] f32 or bf16.
+ *   layout  of the N weight rows: MOE_LAYOUT_ROWS, quantised rows as moe_quantize_mx gives them; or MOE_LAYOUT_TILE16, the
+ *           codes [N, K / 2] and scales [N, K / 32] of a packed MXFP4_E8M0 bank (then N a multiple of 16). */
+int moe_mx_mm(const void *xq, const void *xs, const void *wq, const void *ws, int layout, int M, int N, int K,
+              void *y, int out_dtype, void *stream);
+
+/* The same by expert: the E * N weight rows of all experts, wq [E, N, K / 2] with ws [ceil(K / 128), E * N, 4] (ROWS), or
+ * ws [E, N, K / 32] (TILE16: a bank's gate_up and gate_up_scale with N = 2I and K = H, or its down and down_scale with
+ * N = H and K = I).  Row ranges, expected_rows, limits and rows of no expert as for the grouped products. */
+int moe_grouped_mx_mm(const void *xq, const void *xs, const void *wq, const void *ws, int layout,
+                      const int32_t *offsets, const int32_t *counts, int E, int M, int expected_rows, int N,
+                      int K, void *y, int out_dtype, void *stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 
 const char *moe_status_string(int status); /* static text for a status code */

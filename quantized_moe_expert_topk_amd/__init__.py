@@ -13,4 +13,5 @@ from .api import (AlignOut, DeviceBank, MoeLayer, alloc_align, choose_block_m, m
                   moe_route_from_logits, moe_route_workspace_bytes, moe_workspace_bytes)
 from .grouped import (moe_block_mm, moe_grouped_block_mm, moe_grouped_mm, moe_grouped_mm_dgrad,  # noqa: F401
                       moe_grouped_mm_wgrad, moe_quantize_blocks)
+from .mx import moe_dequantize_mx, moe_grouped_mx_mm, moe_mx_mm, moe_quantize_mx  # noqa: F401
 from .rows import moe_combine_rows, moe_combine_rows_grad, moe_gather_rows, moe_pair_slots  # noqa: F401

@@ -29,6 +29,7 @@ EXPORTS = ("moe_route", "moe_route_workspace_bytes", "moe_route_from_logits", "m
            "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad", "moe_quantize_blocks",
            "moe_block_mm", "moe_grouped_block_mm",
            "moe_pair_slots", "moe_gather_rows", "moe_combine_rows", "moe_combine_rows_grad",
+           "moe_quantize_mx", "moe_dequantize_mx", "moe_mx_mm", "moe_grouped_mx_mm",
            "moe_status_string", "moe_last_error")
 
 
@@ -100,6 +101,10 @@ def lib() -> ctypes.CDLL:
         L.moe_gather_rows.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp]
         L.moe_combine_rows.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
         L.moe_combine_rows_grad.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_quantize_mx.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_dequantize_mx.argtypes = [vp, vp, i32, i32, vp, i32, vp]
+        L.moe_mx_mm.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp]
+        L.moe_grouped_mx_mm.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp]
         L.moe_status_string.argtypes = [i32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = []

@@ -167,4 +167,25 @@ hipError_t launch_combine_rows_grad(const void *dout, bool dout_f32, const void 
                                     const float *weights, int T, int k, int M, int H, void *drows, float *dweights,
                                     hipStream_t s);
 
+// ---- MXFP4: quantiser (mx.hip) and products (mx_mm.hip, mx_few.hip)
+
+// Scales [ceil(K / 128), rows, 4] bytes, four blocks of a row together; a packed bank's weights (tile16) have them as
+// the bank does.
+struct MxArgs {
+  const uint8_t *x, *xs, *w, *ws;
+  void *out;
+  Groups g;
+  int N, K;
+  long long w_rows;  // E * N
+  int tile16;
+  int p_tiles, q_run;  // set by the launcher (as in ProductArgs)
+};
+
+hipError_t launch_quantize_mx(const uint16_t *x, const int32_t *slots, int T, int k, int M, int K, uint8_t *q,
+                              uint8_t *scale, hipStream_t s);
+hipError_t launch_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, int K, void *y, bool out_f32, hipStream_t s);
+// rows: as for launch_grouped_mm.
+hipError_t launch_mx_mm(const MxArgs &a, int rows, bool out_bf16, hipStream_t s);
+hipError_t launch_mx_few(MxArgs a, bool out_bf16, hipStream_t s);
+
 }  // namespace qmoe
