@@ -178,7 +178,7 @@ struct MxArgs {
   int N, K;
   long long w_rows;  // E * N
   int tile16;
-  int p_tiles, q_run;  // set by the launcher (as in ProductArgs)
+  int p_tiles, q_run, write_through;  // set by the launcher (as in ProductArgs)
 };
 
 hipError_t launch_quantize_mx(const uint16_t *x, const int32_t *slots, int T, int k, int M, int K, uint8_t *q,

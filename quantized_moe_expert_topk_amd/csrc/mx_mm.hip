@@ -1,8 +1,478 @@
-// mx_mm.hip -- the MXFP4 products, dense and grouped by expert, gfx950.
+// mx_mm.hip -- the tiled MXFP4 products, dense and grouped by expert, gfx950.
+//
+//   y[r, n] = sum_b 2^(xs[r, b] + ws[n, b] - 254) sum_{k in block b} xq[r, k] wq[n, k]
+//
+// The pipeline of product_dev.h (persistent workgroups, operands loaded straight to LDS NS stages ahead across the tiles'
+// borders, fragments read one step ahead of the products), with p along n and q along the rows.  A stage is 128 bytes of
+// each row, 256 columns, and their scales.
+#include <algorithm>
+#include <iterator>
+#include <type_traits>
+#include <utility>
+
 #include "mx_dev.h"
+#include "product_dev.h"
 
 namespace qmoe {
 
-hipError_t launch_mx_mm(const MxArgs &a, int, bool out_bf16, hipStream_t s) { return launch_mx_few(a, out_bf16, s); }
+// Weights of a packed bank: a stage's part of 16 rows is 2 KB in one piece, [8 units of 16 bytes][16 rows], and lies so in
+// LDS, loaded in contiguous runs.  Fragment p of a wave's TP takes rows p, TP + p, 2 TP + p, ...: their scales of one block
+// are then the bytes of one operand.  Of 16 rows' tile t, row r lies at r with its last bits (those below TP) turned by t: the
+// 16 lanes that a ds_read_b128 serves together read 256 bytes of all banks.
+template <int R, int THREADS, int TP>
+struct PackedTile {
+  static constexpr int kBytes = R * KB, NL = R * (KB / 16) / THREADS;
+  static_assert(THREADS / 128 % TP == 0, "one turn for all of a thread's tiles");
+  uint32_t voff, step;
+  int unit;
+  __device__ __forceinline__ static uint32_t turned(uint32_t r, uint32_t t) { return (r & ~(TP - 1u)) | ((r + t) & (TP - 1u)); }
+  __device__ __forceinline__ void init(uint32_t pitch) {
+    const uint32_t tid = threadIdx.x, t = tid / 128;
+    unit = tid / 16 % 8;
+    voff = t * 16 * pitch + unit * 256 + turned(tid % 16, TP - t % TP) * 16;
+    step = THREADS / 8 * pitch;
+  }
+  template <bool NT>
+  __device__ __forceinline__ void load(const i32x4g &rs, uint32_t dst, int j, int left) const {
+    const uint32_t at = unit < left ? voff + j * step : kNowhere, to = dst + j * THREADS * 16;
+    if constexpr (NT)
+      load_to_lds16_nt(rs, at, to);
+    else
+      load_to_lds16(rs, at, to);
+  }
+};
+
+// One output tile.
+struct MxTile {
+  int e, p0, q0, rows;  // rows: output rows q0, q0 + 1, ... that exist
+};
+
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool TILE16, bool OUT_BF16>
+__global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
+  constexpr int W = WP * WQ, THREADS = 64 * W, TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  using ATile = std::conditional_t<TILE16, PackedTile<BP, THREADS, TP>, RowTile<BP, THREADS>>;
+  using BTile = RowTile<BQ, THREADS>;
+  // Scales in LDS, a dword for each row: of the weights' first group of 128 columns, of their second, then of x.  A dword is
+  // four blocks of a row; of a packed bank's weights, one block of four rows, 16 rows x 4 blocks after one another.  Four
+  // waves load a group each, 16 bytes a lane (a load to LDS takes its 20 cycles of the CU whatever it brings: with 4 bytes
+  // a lane, 16 of them a stage, 8192 x 4096 x 4096 took 71 us).
+  constexpr int CODES = ATile::kBytes + BTile::kBytes, STAGE = CODES + (BP + BQ) * 8;
+  constexpr int LOADS = ATile::NL + BTile::NL + 1;  // per thread and stage
+  static_assert(W >= 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  __shared__ int32_t first[kMaxExperts + 1];
+
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave % WP, wq = wave / WP, h = lane >> 5, r32 = lane & 31;
+  const int units = a.K / 32;
+  const uint32_t pitch = (uint32_t)units * 16;
+
+  int q_total = (a.g.M + BQ - 1) / BQ;
+  if (a.g.offsets) q_total = make_tile_table<THREADS>(a.g, BQ, first);
+
+  // The tiles' order and the XCDs' shares of it are those of k_product.  (A quotient is computed in vector registers; what
+  // comes of it has to be scalar again, for the loads' resources.)
+  const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  auto locate = [&](int &t, MxTile &o) __attribute__((always_inline)) {
+    const int band = a.q_run * a.p_tiles;
+    for (;; t += gridDim.x) {
+      const int bq = uniform(t / band);
+      if (bq * a.q_run >= q_total) return false;
+      const int r = t - bq * band, pt = uniform(r / a.q_run), qt = bq * a.q_run + r - pt * a.q_run;
+      if (qt >= q_total) continue;
+      o.p0 = pt * BP;
+      o.e = 0;
+      int lo = 0, n = a.g.M, f = 0;
+      if (a.g.offsets) {
+        o.e = uniform(expert_of_tile(first, a.g.E, qt));
+        f = uniform(first[o.e]);
+        group_range_uniform(a.g, o.e, lo, n);
+        lo = uniform(lo);
+        n = uniform(n);
+      }
+      o.q0 = lo + (qt - f) * BQ;
+      o.rows = min(BQ, n - (qt - f) * BQ);
+      return true;
+    }
+  };
+
+  // ---- the loads
+  ATile at;
+  BTile bt;
+  if constexpr (TILE16)
+    at.init(pitch);
+  else
+    at.init(pitch, false);
+  bt.init(pitch, false);
+  i32x4g ra{}, rb{}, rs{};  // what is left of the tile's codes of w and x, and of the scales that this wave loads
+  int left = 0;             // 16-byte units of the contraction of the tile being loaded
+  int lt = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+  const bool of_w = wave < 2;
+  const int half = wave & 1;  // the group of 128 columns whose scales this wave loads (waves 4 and up: none)
+  const auto advance = [](i32x4g &r, uint64_t by) __attribute__((always_inline)) {
+    const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + by;
+    r[0] = (int)(uint32_t)at;
+    r[1] = (int)(uint32_t)(at >> 32);
+  };
+  const bool packed = TILE16 && of_w;
+  const uint64_t step_s = packed ? 128 : (uint64_t)(of_w ? a.w_rows : (long long)a.g.M) * 8;
+  auto start = [&](const MxTile &o) __attribute__((always_inline)) {
+    left = units;
+    const size_t w_row = (size_t)o.e * a.N + o.p0;
+    const int cols = min(BP, a.N - o.p0);
+    ra = range_rsrc(a.w + w_row * pitch, cols * pitch);
+    rb = range_rsrc(a.x + (size_t)o.q0 * pitch, o.rows * pitch);
+    if (packed)  // the scales of `cols` rows from the half's first block on
+      rs = range_rsrc(a.ws + w_row * units + half * 64, max(cols * units - half * 64, 0));
+    else if (of_w)
+      rs = range_rsrc(a.ws + (half * (size_t)a.w_rows + w_row) * 4, half * 4 < left ? cols * 4 : 0);
+    else
+      rs = range_rsrc(a.xs + (half * (size_t)a.g.M + o.q0) * 4, half * 4 < left ? o.rows * 4 : 0);
+  };
+  auto find_next = [&]() __attribute__((always_inline)) {
+    lt += gridDim.x;
+    MxTile o;
+    if (locate(lt, o)) {
+      start(o);
+    } else {  // the loads past the last tile fetch nothing
+      left = 0;
+      ra[2] = rb[2] = rs[2] = 0;
+    }
+  };
+  const uint32_t lds0 = lds_addr(lds), lds_wave = lds0 + wave * 1024;
+  const uint32_t s_off = packed ? (lane >> 2) * 16 * units + (lane & 3) * 16 : lane * 16;
+  const int s_block = packed ? half * 4 + (lane & 3) : 0;  // packed: past a row's last block lie the next 16 rows' scales
+  const int s_lanes = wave < 2 ? BP / 4 : wave < 4 ? BQ / 4 : 0;
+  const uint64_t s_mask = s_lanes == 64 ? ~0ull : (1ull << s_lanes) - 1;
+  const uint32_t s_dst = lds0 + CODES + (of_w ? half * BP : 2 * BP + half * BQ) * 4;
+  auto load = [&](int slot, int i) __attribute__((always_inline)) {
+    const uint32_t d = lds_wave + slot * STAGE;
+    if (i == 0)
+      load_to_lds16_masked(rs, s_block < left ? s_off : kNowhere, s_dst + slot * STAGE, s_mask);
+    else if (i <= ATile::NL)
+      at.template load<NT>(ra, d, i - 1, left);
+    else
+      bt.load(rb, d + ATile::kBytes, i - 1 - ATile::NL, left);
+  };
+  auto close = [&]() __attribute__((always_inline)) {
+    constexpr int STEP_A = TILE16 ? KB * 16 : KB;
+    left -= KB / 16;
+    advance(ra, STEP_A);
+    advance(rb, KB);
+    advance(rs, step_s);
+    ra[2] -= STEP_A;
+    rb[2] -= KB;
+    rs[2] = packed ? max(rs[2] - 128, 0) : half * 4 < left ? rs[2] : 0;
+    if (left <= 0) find_next();
+  };
+
+  // ---- the products
+  MxTile o;
+  int ct = lt;
+  if (!locate(ct, o)) return;
+  lt = ct;
+  start(o);
+  f32x16_t acc[TP][TQ];
+  // Step ks multiplies the units ks (lanes 0..31) and 4 + ks (lanes 32..63) of a stage: the scales of a lane's four steps are
+  // then the bytes of one dword, which the instruction picks from (packed banks: those of the fragments).
+  constexpr int NKS = 4, NM = TP * TQ, NR = TP + TQ;
+  uint32_t a_at[TILE16 ? TP : NKS], b_at[NKS];  // a_at by fragment (packed), or by step
+#pragma unroll
+  for (int ks = 0; ks < NKS; ks++) {  // (of fragment 0: the swizzle repeats every 16 rows)
+    const uint32_t u = ((4 * h + ks) ^ row_swz(r32)) * 16;
+    if constexpr (!TILE16) a_at[ks] = (wp * TP * 32 + r32) * KB + u;
+    b_at[ks] = ATile::kBytes + (wq * TQ * 32 + r32) * KB + u;
+  }
+  if constexpr (TILE16) {
+    const uint32_t t = wp * TP * 2 + TP * r32 / 16;
+#pragma unroll
+    for (int p = 0; p < TP; p++) a_at[p] = t * 16 * KB + 4 * h * 256 + ATile::turned(TP * r32 % 16 + p, t) * 16;
+  }
+  const uint32_t sa_at = CODES + h * BP * 4 + wp * TP * 128 + (TILE16 ? TP * r32 / 16 * 64 + TP * r32 % 16 : r32 * 4);
+  const uint32_t sb_at = CODES + BP * 8 + h * BQ * 4 + wq * TQ * 128 + r32 * 4;
+  uint4 af[2][TP], bf[2][TQ];
+  uint32_t sa[2][TILE16 ? 1 : TP], sb[TQ], sb_next[TQ];  // sa: of a step (packed banks), or of this stage and the next one
+  // Before a stage's last step the waves meet: its slot has been read, and the next one is loaded.  The slot's loads then go
+  // out beside the four steps up to the next meeting, the first FIRST of them beside the first; with two slots, which leave
+  // one stage of time, all of them.
+  constexpr int FIRST = NS > 2 ? LOADS / NKS : LOADS;
+  int slot = 0, fill = NS - 1, stored = 0;
+  constexpr int STORES = TP * TQ * (OUT_BF16 ? 2 : 4);
+  auto wait_loads = [&]() __attribute__((always_inline)) {
+    if (stored)  // (stores, and loads in front of the newest NS - 2 stages', end in order)
+      wait_vm<STORES + (NS - 2) * LOADS>();
+    else
+      wait_vm<(NS - 2) * LOADS>();
+    stored = 0;
+  };
+  auto read = [&](int sl, int ks, int to, int i) __attribute__((always_inline)) {
+    const uint8_t *t = lds + sl * STAGE;
+    if (i < TQ) {
+      bf[to][i] = *reinterpret_cast<const uint4 *>(t + b_at[ks] + i * 32 * KB);
+    } else {
+      const int p = i - TQ;
+      if constexpr (TILE16) {
+        af[to][p] = *reinterpret_cast<const uint4 *>(t + a_at[p] + ks * 256);
+        const uint8_t *s = t + sa_at + ks * 16;
+        if (p == 0) sa[to][0] = TP == 4 ? *reinterpret_cast<const uint32_t *>(s) : TP == 2 ? *reinterpret_cast<const uint16_t *>(s) : *s;
+      } else {
+        af[to][p] = *reinterpret_cast<const uint4 *>(t + a_at[ks] + p * 32 * KB);
+      }
+    }
+  };
+  auto read_scales = [&](int sl) __attribute__((always_inline)) {
+    const uint8_t *t = lds + sl * STAGE;
+#pragma unroll
+    for (int q = 0; q < TQ; q++) sb_next[q] = *reinterpret_cast<const uint32_t *>(t + sb_at + q * 128);
+    if constexpr (!TILE16) {
+#pragma unroll
+      for (int p = 0; p < TP; p++) sa[1][p] = *reinterpret_cast<const uint32_t *>(t + sa_at + p * 128);
+    }
+  };
+  auto use_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < TQ; q++) sb[q] = sb_next[q];
+    if constexpr (!TILE16) {
+#pragma unroll
+      for (int p = 0; p < TP; p++) sa[0][p] = sa[1][p];
+    }
+  };
+  // Products may not move past this point: without it they sink behind the next barrier, and the matrix core idles until it.
+  auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < TP; p++)
+#pragma unroll
+      for (int q = 0; q < TQ; q++) asm volatile("" : "+v"(acc[p][q]));
+  };
+  auto stage = [&]() __attribute__((always_inline)) {
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+    static_for<NKS>([&](auto ks) __attribute__((always_inline)) {
+      constexpr bool last = ks == NKS - 1;
+      constexpr int cur = ks & 1;
+      if constexpr (last) {
+        wait_loads();
+        barrier_only();
+        fill = slot;
+        read_scales(next);
+      }
+      constexpr int TICKS = NM > NR ? NM : NR;
+      static_for<TICKS>([&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < NM) {
+          constexpr int p = i / TQ, q = i % TQ;
+          acc[p][q] = mfma32_mx<TILE16 ? p : ks, ks>(af[cur][p], bf[cur][q], sa[TILE16 ? cur : 0][TILE16 ? 0 : p], sb[q], acc[p][q]);
+        }
+        constexpr int r0 = i * NR / TICKS, r1 = (i + 1) * NR / TICKS;
+        static_for<r1 - r0>([&](auto r) __attribute__((always_inline)) {
+          read(last ? next : slot, last ? 0 : ks + 1, cur ^ 1, r0 + r);
+        });
+        constexpr int SPAN = NS > 2 ? NKS : 1, at = (ks + 1) % NKS * TICKS + i;  // ticks from the meeting on
+        constexpr int j0 = at >= SPAN * TICKS ? LOADS : at * LOADS / (SPAN * TICKS);
+        constexpr int j1 = at >= SPAN * TICKS ? LOADS : (at + 1) * LOADS / (SPAN * TICKS);
+        static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(fill, j0 + j); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      pin();
+      if constexpr (ks == (NS > 2 ? NKS - 2 : NKS - 1)) close();
+      if constexpr (last) use_scales();
+    });
+    slot = next;
+  };
+
+  // D register j of a lane: i = 8 (j / 4) + 4 h + j % 4 of fragment p, row lane % 32 of q.  i of fragment p is column 32 p + i
+  // of the wave's, or TP i + p (packed).  Lanes trade pieces of 16 bytes, so that four of them hold 64 consecutive bytes of
+  // a row: a wave issues exactly STORES stores of 16 bytes a lane where rows are whole such pieces (N a multiple of 8, or
+  // of 4 in fp32), whatever part of the tile exists (the resource refuses the rest).
+  auto store = [&]() __attribute__((always_inline)) {
+    constexpr uint32_t OS = OUT_BF16 ? 2 : 4;
+    constexpr int PIECE = 16 / OS;
+    constexpr bool MIXED = TILE16 && TP > 1;
+    const uint32_t out_pitch = (uint32_t)a.N * OS;
+    const rsrc_t ro = make_rsrc(static_cast<uint8_t *>(a.out) + (size_t)o.q0 * out_pitch, o.rows * out_pitch);
+    const int c0 = o.p0 + wp * TP * 32, s = lane >> 4 & 1, r16 = lane & 15;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    // what a lane and the one 16 (32) lanes away hold of x and y, so that the first ends with both x, the second with both y
+    const auto trade16 = [](u32x4 &x, u32x4 &y) __attribute__((always_inline)) {
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const auto v = __builtin_amdgcn_permlane16_swap(x[w], y[w], false, false);
+        x[w] = v[0];
+        y[w] = v[1];
+      }
+    };
+    const auto trade32 = [](u32x4 &x, u32x4 &y) __attribute__((always_inline)) {
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const auto v = __builtin_amdgcn_permlane32_swap(x[w], y[w], false, false);
+        x[w] = v[0];
+        y[w] = v[1];
+      }
+    };
+    const auto put = [&](auto policy) __attribute__((always_inline)) {
+      const auto store16 = [&](const u32x4 &v, int row, int c) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)(c < a.N ? row * out_pitch + c * OS : kNowhere), 0, policy());
+      };
+#pragma unroll
+      for (int q = 0; q < TQ; q++) {
+        const int row = (wq * TQ + q) * 32 + r16;
+        // piece n of a lane, in the columns' order: PIECE elements from e(PIECE n) on
+        const auto element = [&](int n) __attribute__((always_inline)) {
+          return MIXED ? acc[n % TP][q][n / TP] : acc[n / 16][q][n % 16];
+        };
+        const auto piece = [&](int n) __attribute__((always_inline)) {
+          u32x4 v;
+#pragma unroll
+          for (int w = 0; w < 4; w++)
+            if constexpr (OUT_BF16)
+              v[w] = __builtin_bit_cast(uint32_t, pack_bf16(element(8 * n + 2 * w), element(8 * n + 2 * w + 1)));
+            else
+              v[w] = __float_as_uint(element(4 * n + w));
+          return v;
+        };
+        constexpr int RUN = MIXED ? 4 * TP : 4;  // consecutive columns of a lane; the lane 32 away has the RUN after them
+        if constexpr (RUN * OS == 8) {           // half a piece: two runs to a piece, then rows
+#pragma unroll
+          for (int n = 0; n < TP * 2; n += 2) {
+            u32x4 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              const u32x4 v = piece(n + i);  // runs 2 n and 2 n + 1
+              const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+              const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+              x[i] = u32x4{lo[0], hi[0], lo[1], hi[1]};  // columns 16 (n + i) + 8 h
+            }
+            trade16(x[0], x[1]);
+#pragma unroll
+            for (int i = 0; i < 2; i++) store16(x[i], row + 16 * i, c0 + 16 * (n + s) + 8 * h);
+          }
+        } else if constexpr (RUN == PIECE) {  // one piece
+#pragma unroll
+          for (int n = 0; n < TP * 16 / PIECE; n += 2) {
+            u32x4 x = piece(n), y = piece(n + 1);
+            trade16(x, y);
+            const int c = c0 + 2 * RUN * (n + s) + RUN * h;
+            store16(x, row, c);
+            store16(y, row + 16, c);
+          }
+        } else if constexpr (RUN == 2 * PIECE) {
+#pragma unroll
+          for (int n = 0; n < TP * 16 / PIECE; n += 2) {
+            u32x4 x = piece(n), y = piece(n + 1);
+            trade16(x, y);
+            const int c = c0 + 2 * RUN * (n / 2) + RUN * h + PIECE * s;
+            store16(x, row, c);
+            store16(y, row + 16, c);
+          }
+        } else {
+          static_assert(RUN * OS <= 16 || RUN <= 4 * PIECE, "runs of at most four pieces");
+#pragma unroll
+          for (int n = 0; n < TP * 16 / PIECE; n += 4) {
+            u32x4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[i] = piece(n + i);
+            trade16(x[0], x[1]);
+            trade16(x[2], x[3]);
+            trade32(x[0], x[2]);
+            trade32(x[1], x[3]);
+            // x[i]: piece 2 h + s of the lane that has row 16 (i % 2) and run 2 (n / 4) + i / 2
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              store16(x[i], row + 16 * (i % 2), c0 + RUN * (2 * (n / 4) + i / 2) + PIECE * (2 * h + s));
+          }
+        }
+      }
+    };
+    if (a.N % (OUT_BF16 ? 8 : 4) == 0) {
+      if (a.write_through)
+        put(std::integral_constant<int, kWriteThrough>{});
+      else
+        put(std::integral_constant<int, 0>{});
+      stored = 1;
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < TQ; q++) {
+      const uint32_t row = ((wq * TQ + q) * 32 + r32) * out_pitch;
+#pragma unroll
+      for (int p = 0; p < TP; p++)
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+          const int i = 8 * (j / 4) + 4 * h + j % 4, c = c0 + (MIXED ? TP * i + p : p * 32 + i);
+          const int off = (int)(c < a.N ? row + c * OS : kNowhere);
+          if constexpr (OUT_BF16)
+            __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(acc[p][q][j]), ro, off, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[p][q][j]), ro, off, 0, 0);
+        }
+    }
+  };
+
+#pragma unroll
+  for (int s = 0; s < NS; s++) {
+#pragma unroll
+    for (int i = 0; i < (s < NS - 1 ? LOADS : FIRST); i++) load(s, i);
+    if (s < NS - 1 || FIRST == LOADS) close();
+  }
+  wait_vm<(NS - 2) * LOADS + FIRST>();
+  barrier_only();
+#pragma unroll
+  for (int i = 0; i < NR; i++) read(0, 0, 0, i);
+  read_scales(0);
+  use_scales();
+  const int n_stages = (units + KB / 16 - 1) / (KB / 16);
+  for (;;) {
+#pragma unroll
+    for (int p = 0; p < TP; p++)
+#pragma unroll
+      for (int q = 0; q < TQ; q++)
+#pragma unroll
+        for (int j = 0; j < 16; j++) acc[p][q][j] = 0.f;
+    for (int s = 0; s < n_stages; s++) stage();
+    store();
+    ct += gridDim.x;
+    if (!locate(ct, o)) break;
+  }
+  wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
+}
+
+namespace {
+
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT>
+hipError_t run_mx(MxArgs a, bool out_bf16, hipStream_t s) {
+  a.p_tiles = (a.N + BP - 1) / BP;
+  const long long q = a.g.offsets ? a.g.M / BQ + std::min(a.g.E, a.g.M) : (a.g.M + BQ - 1) / BQ;  // the most there can be
+  a.q_run = (int)std::max(1LL, std::min(4LL, q));
+  const long long pitch = (long long)a.N * (out_bf16 ? 2 : 4);
+  a.write_through = stores_go_through(a.out, (double)a.g.M * pitch, pitch);
+  const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
+  if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
+  constexpr int LDS = NS * ((BP + BQ) * (KB + 8)) + kMaxExperts * 4 + 256;
+  constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 2 : 1);
+  const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
+  const auto run = [&](auto packed, auto bf16) {
+    k_mx_product<BP, BQ, WP, WQ, NS, NT, decltype(packed)::value, decltype(bf16)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
+  };
+  if (a.tile16)
+    out_bf16 ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
+  else
+    out_bf16 ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// The product with tile t of kMxTiles.
+template <size_t... I>
+static hipError_t run_mx_tile(int t, const MxArgs &a, bool out_bf16, hipStream_t s, std::index_sequence<I...>) {
+  hipError_t e = hipErrorInvalidValue;
+  (void)((t == (int)I && (e = run_mx<kMxTiles[I].bp, kMxTiles[I].bq, kMxTiles[I].wp, kMxTiles[I].wq, kMxTiles[I].stages,
+                                     kMxTiles[I].nt>(a, out_bf16, s), true)) || ...);
+  return e;
+}
+
+hipError_t launch_mx_mm(const MxArgs &a, int rows, bool out_bf16, hipStream_t s) {
+  const int t = choose_mx(a, rows);
+  if (t == kFewRows) return launch_mx_few(a, out_bf16, s);
+  return run_mx_tile(t, a, out_bf16, s, std::make_index_sequence<std::size(kMxTiles)>{});
+}
 
 }  // namespace qmoe
