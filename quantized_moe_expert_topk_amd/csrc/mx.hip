@@ -4,8 +4,10 @@
 //
 // Memory bounds both.  A wave takes 512 columns of one row, 8 a lane: 4 lanes hold a block.
 #include <algorithm>
+#include <type_traits>
 
 #include "grouped_dev.h"
+#include "tiles.h"
 
 namespace qmoe {
 namespace {
@@ -19,9 +21,20 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// Non-temporal where rows are whole lines (whole_lines(): rows.hip says why).  8192 x 2048 to 8 experts each, us: codes 29
+// without, 23 with; the values of the 65536 rows 81, 64.
+template <bool NT, class V>
+__device__ __forceinline__ void store_vec(V *p, V v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 }  // namespace
 
 // slots NULL: row t of x is row t of q (k is 1).  Else a token is quantised once and written to each of its rows.
+template <bool NT>
 __global__ __launch_bounds__(64 * kWaves) void k_quantize_mx(const uint16_t *x, const int32_t *slots, int T, int k, int M,
                                                              int K, uint8_t *q, uint8_t *scale) {
   const int lane = lane_id(), c = blockIdx.y * 512 + lane * 8;
@@ -55,14 +68,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_quantize_mx(const uint16_t *x, 
       for (int j = 0; j < min(64, k - j0); j++) {
         const int s = __builtin_amdgcn_readlane(sl, j);
         if ((uint32_t)s >= (uint32_t)M || c >= K) continue;
-        *reinterpret_cast<uint32_t *>(q + ((size_t)s * K + c) / 2) = codes;
+        store_vec<NT>(reinterpret_cast<uint32_t *>(q + ((size_t)s * K + c) / 2), codes);
         if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(scale + ((size_t)(c / 128) * M + s) * 4) = four;
       }
     }
   }
 }
 
-template <bool OUT_F32>
+template <bool OUT_F32, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, int K,
                                                                uint8_t *y) {
   const int c = blockIdx.y * 512 + lane_id() * 8;
@@ -77,13 +90,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q,
     const size_t at = (size_t)r * K + c;
     if constexpr (OUT_F32) {
       f32x4_t *o = reinterpret_cast<f32x4_t *>(y + at * 4);
-      o[0] = f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s};
-      o[1] = f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s};
+      store_vec<NT>(o, f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s});
+      store_vec<NT>(o + 1, f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s});
     } else {
-      frag8 o;
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      u32x4 o;
 #pragma unroll
-      for (int i = 0; i < 4; i++) o.h[i] = pack_bf16(f[i][0] * s, f[i][1] * s);
-      *reinterpret_cast<uint4 *>(y + at * 2) = o.q;
+      for (int i = 0; i < 4; i++) o[i] = __builtin_bit_cast(uint32_t, pack_bf16(f[i][0] * s, f[i][1] * s));
+      store_vec<NT>(reinterpret_cast<u32x4 *>(y + at * 2), o);
     }
   }
 }
@@ -91,16 +105,23 @@ __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q,
 hipError_t launch_quantize_mx(const uint16_t *x, const int32_t *slots, int T, int k, int M, int K, uint8_t *q,
                               uint8_t *scale, hipStream_t s) {
   const dim3 grid(std::min((T + kWaves - 1) / kWaves, kMaxGroups), (K + 511) / 512);
-  k_quantize_mx<<<grid, 64 * kWaves, 0, s>>>(x, slots, T, k, M, K, q, scale);
+  if (whole_lines(q, K / 2))
+    k_quantize_mx<true><<<grid, 64 * kWaves, 0, s>>>(x, slots, T, k, M, K, q, scale);
+  else
+    k_quantize_mx<false><<<grid, 64 * kWaves, 0, s>>>(x, slots, T, k, M, K, q, scale);
   return hipGetLastError();
 }
 
 hipError_t launch_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, int K, void *y, bool out_f32, hipStream_t s) {
   const dim3 grid(std::min((M + kWaves - 1) / kWaves, kMaxGroups), (K + 511) / 512);
+  const auto run = [&](auto f32, auto nt) {
+    k_dequantize_mx<decltype(f32)::value, decltype(nt)::value><<<grid, 64 * kWaves, 0, s>>>(q, scale, M, K, static_cast<uint8_t *>(y));
+  };
+  const bool nt = whole_lines(y, K * (out_f32 ? 4LL : 2LL));
   if (out_f32)
-    k_dequantize_mx<true><<<grid, 64 * kWaves, 0, s>>>(q, scale, M, K, static_cast<uint8_t *>(y));
+    nt ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
   else
-    k_dequantize_mx<false><<<grid, 64 * kWaves, 0, s>>>(q, scale, M, K, static_cast<uint8_t *>(y));
+    nt ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 

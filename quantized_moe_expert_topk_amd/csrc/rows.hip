@@ -10,9 +10,12 @@
 #include <type_traits>
 
 #include "grouped_dev.h"
+#include "tiles.h"
 
 namespace qmoe {
 namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;          // of a workgroup
 constexpr int kMaxGroups = 1 << 20;  // workgroups along x; more tokens take several turns each
@@ -22,6 +25,17 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 template <class T>
 __device__ __forceinline__ T read_lane(T v, int lane) {
   return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// Stores are non-temporal where rows are whole lines (whole_lines()): nothing here reads them again.  8192 tokens of 2048
+// bf16 to 8 of 256 experts, us: gather 61 without, 53 with; combine 66, 63; gradients 120, 115.  Rows of 1040 bytes 14
+// without, 21 with: lines that two rows share are then written in parts.
+template <bool NT, class V>
+__device__ __forceinline__ void store_vec(V *p, V v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
 }
 
 // N consecutive elements of one row, 16 bytes in memory per 4 (fp32) or 8 (bf16).
@@ -41,7 +55,7 @@ __device__ __forceinline__ void unpack(const uint4 (&q)[F32 ? N / 4 : N / 8 > 0 
 }
 
 // N elements at p, which is aligned to their bytes, as fp32; and back.
-template <bool F32, int N>
+template <bool F32, int N, bool NT = false>
 __device__ __forceinline__ void load_row(const void *p, float (&f)[N]) {
   if constexpr (!F32 && N == 4) {
     const uint2 v = *static_cast<const uint2 *>(p);
@@ -50,24 +64,25 @@ __device__ __forceinline__ void load_row(const void *p, float (&f)[N]) {
   } else {
     uint4 q[F32 ? N / 4 : N / 8];
 #pragma unroll
-    for (int i = 0; i < (F32 ? N / 4 : N / 8); i++) q[i] = static_cast<const uint4 *>(p)[i];
+    for (int i = 0; i < (F32 ? N / 4 : N / 8); i++) {
+      const u32x4_t *v = static_cast<const u32x4_t *>(p) + i;
+      q[i] = __builtin_bit_cast(uint4, NT ? __builtin_nontemporal_load(v) : *v);
+    }
     unpack<F32, N>(q, f);
   }
 }
-template <bool F32, int N>
+template <bool F32, int N, bool NT>
 __device__ __forceinline__ void store_row(void *p, const float (&f)[N]) {
   if constexpr (F32) {
 #pragma unroll
     for (int i = 0; i < N / 4; i++)
-      static_cast<f32x4_t *>(p)[i] = f32x4_t{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+      store_vec<NT>(static_cast<f32x4_t *>(p) + i, f32x4_t{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]});
   } else {
-    uint32_t u[N / 2];
+    typedef uint32_t u32xn __attribute__((ext_vector_type(N / 2)));
+    u32xn u;
 #pragma unroll
     for (int i = 0; i < N / 2; i++) u[i] = __builtin_bit_cast(uint32_t, pack_bf16(f[2 * i], f[2 * i + 1]));
-    if constexpr (N == 4)
-      *static_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
-    else
-      *static_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    store_vec<NT>(static_cast<u32xn *>(p), u);
   }
 }
 
@@ -105,33 +120,28 @@ __global__ __launch_bounds__(256) void k_pair_slots(const int32_t *ids, int P, c
   slots[f] = s;
 }
 
-// A wave holds U x 1 KB of one token's row and stores it to each of the token's slots.
-template <int U>
-__global__ __launch_bounds__(64 * kWaves) void k_gather_rows(const uint4 *x, int T, int k, const int32_t *slots, int M,
-                                                             uint4 *rows, uint32_t units) {
+// A wave holds 1 KB of one token's row and stores it to each of the token's slots; the waves of a workgroup hold
+// neighbouring ones (with neighbouring tokens' instead, 75 us for 53: rows are then written in parts far apart in time).
+template <bool NT>
+__global__ __launch_bounds__(64 * kWaves) void k_gather_rows(const u32x4_t *x, int T, int k, const int32_t *slots, int M,
+                                                             u32x4_t *rows, uint32_t units) {
   const int lane = lane_id();
-  const uint32_t u0 = blockIdx.y * 64 * U + lane;
-  for (int64_t t = blockIdx.x * kWaves + wave_id(); t < T; t += gridDim.x * kWaves) {
-    uint4 v[U];
-#pragma unroll
-    for (int i = 0; i < U; i++)
-      if (u0 + 64 * i < units) v[i] = x[(size_t)t * units + u0 + 64 * i];
+  const uint32_t u = (blockIdx.y * kWaves + wave_id()) * 64 + lane;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    u32x4_t v = {};
+    if (u < units) v = x[t * units + u];
     for (int j0 = 0; j0 < k; j0 += 64) {
       const int sl = lane < k - j0 ? slots[t * k + j0 + lane] : -1;
       for (int j = 0; j < min(64, k - j0); j++) {
         const int s = read_lane(sl, j);
-        if ((uint32_t)s >= (uint32_t)M) continue;
-        uint4 *to = rows + (size_t)s * units + u0;
-#pragma unroll
-        for (int i = 0; i < U; i++)
-          if (u0 + 64 * i < units) to[64 * i] = v[i];
+        if ((uint32_t)s < (uint32_t)M && u < units) store_vec<NT>(rows + (size_t)s * units + u, v);
       }
     }
   }
 }
 
 // A wave owns 16 bytes a lane of one output row; the loads of eight pair rows are in flight at once.
-template <bool ROWS_F32, bool OUT_F32>
+template <bool ROWS_F32, bool OUT_F32, bool NT, bool NT_LOADS>
 __global__ __launch_bounds__(64 * kWaves) void k_combine_rows(const uint8_t *rows, const int32_t *slots, const float *weights,
                                                               const uint8_t *add, int T, int k, int M, int H, uint8_t *out) {
   constexpr int N = ROWS_F32 ? 4 : 8, RS = ROWS_F32 ? 4 : 2, OS = OUT_F32 ? 4 : 2, AT_ONCE = 8;
@@ -154,7 +164,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_combine_rows(const uint8_t *row
           const int s = read_lane(sl, j + u);
           const bool there = (uint32_t)s < (uint32_t)M;
           // a resource of no bytes reads zeros
-          q[u][0] = buf_load16(make_rsrc(rows + (size_t)(there ? s : 0) * pitch, there ? pitch : 0), (uint32_t)c * RS);
+          q[u][0] = buf_load16w<NT_LOADS>(make_rsrc(rows + (size_t)(there ? s : 0) * pitch, there ? pitch : 0), (uint32_t)c * RS);
         }
 #pragma unroll
         for (int u = 0; u < AT_ONCE; u++) {
@@ -170,14 +180,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_combine_rows(const uint8_t *row
       if (add)
 #pragma unroll
         for (int i = 0; i < N; i++) acc[i] += more[i];
-      store_row<OUT_F32, N>(out + (t * H + c) * OS, acc);
+      store_row<OUT_F32, N, NT>(out + (t * H + c) * OS, acc);
     }
   }
 }
 
 // A wave per pair: it goes along the pair's row and the token's output gradient, writes the row's gradient, and sums
 // the products; the waves of a token's other pairs find the output gradient in the caches.
-template <bool ROWS_F32, bool DOUT_F32>
+template <bool ROWS_F32, bool DOUT_F32, bool NT, bool NT_LOADS>
 __global__ __launch_bounds__(64 * kWaves) void k_combine_rows_grad(const uint8_t *dout, const uint8_t *rows,
                                                                    const int32_t *slots, const float *weights, int P,
                                                                    int k, int M, int H, uint8_t *drows, float *dweights) {
@@ -197,7 +207,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_combine_rows_grad(const uint8_t
           const int c = c0 + u * 64 * N;
           if (c < H) {
             load_row<DOUT_F32, N>(d + (size_t)c * DS, a[u]);
-            load_row<ROWS_F32, N>(r + (size_t)c * RS, b[u]);
+            load_row<ROWS_F32, N, NT_LOADS>(r + (size_t)c * RS, b[u]);
           }
         }
 #pragma unroll
@@ -210,7 +220,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_combine_rows_grad(const uint8_t
               sum = fmaf(a[u][i], b[u][i], sum);
               g[i] = w * a[u][i];
             }
-            store_row<ROWS_F32, N>(o + (size_t)c * RS, g);
+            store_row<ROWS_F32, N, NT>(o + (size_t)c * RS, g);
           }
         }
       }
@@ -226,16 +236,32 @@ hipError_t launch_pair_slots(const int32_t *ids, int P, const int32_t *sorted, c
   return hipGetLastError();
 }
 
+// f with the flags' values as types.
+template <class F>
+static void with_flags(F &&f) {
+  f();
+}
+template <class F, class... B>
+static void with_flags(F &&f, bool b, B... more) {
+  if (b)
+    with_flags([&](auto... t) { f(std::true_type{}, t...); }, more...);
+  else
+    with_flags([&](auto... t) { f(std::false_type{}, t...); }, more...);
+}
+
+// Pair rows are read non-temporally where they are more than the last cache keeps for the kernel after the one that wrote
+// them (256 MB, outputs and weights besides).  Combine, us without / with: 268 MB 66 / 55, 201 MB 49 / 42, 131 MB 34 / 31,
+// but 67 MB that are still in that cache 18 / 20.
+static bool read_past_caches(long long rows, long long pitch) { return rows * pitch > 100'000'000; }
+
 hipError_t launch_gather_rows(const void *x, int T, int k, const int32_t *slots, int M, void *rows, int row_bytes,
                               hipStream_t s) {
   const uint32_t units = row_bytes / 16;
-  const auto run = [&](auto u) {
-    constexpr int U = decltype(u)::value;
-    const dim3 grid(std::min((T + kWaves - 1) / kWaves, kMaxGroups), (units + 64 * U - 1) / (64 * U));
-    k_gather_rows<U><<<grid, 64 * kWaves, 0, s>>>(static_cast<const uint4 *>(x), T, k, slots, M,
-                                                  static_cast<uint4 *>(rows), units);
-  };
-  run(std::integral_constant<int, 1>{});
+  const dim3 grid(std::min(T, kMaxGroups), (units + 64 * kWaves - 1) / (64 * kWaves));
+  with_flags([&](auto nt) {
+    k_gather_rows<decltype(nt)::value><<<grid, 64 * kWaves, 0, s>>>(static_cast<const u32x4_t *>(x), T, k, slots, M,
+                                                                    static_cast<u32x4_t *>(rows), units);
+  }, whole_lines(rows, row_bytes));
   return hipGetLastError();
 }
 
@@ -243,15 +269,12 @@ hipError_t launch_combine_rows(const void *rows, bool rows_f32, const int32_t *s
                                const void *add, int T, int k, int M, int H, void *out, bool out_f32, hipStream_t s) {
   const int columns = kWaves * 64 * (rows_f32 ? 4 : 8);
   const dim3 grid(std::min(T, kMaxGroups), (H + columns - 1) / columns);
-  const auto run = [&](auto r, auto o) {
-    k_combine_rows<decltype(r)::value, decltype(o)::value><<<grid, 64 * kWaves, 0, s>>>(
+  with_flags([&](auto r, auto o, auto nt, auto ntl) {
+    k_combine_rows<decltype(r)::value, decltype(o)::value, decltype(nt)::value, decltype(ntl)::value><<<grid, 64 * kWaves, 0, s>>>(
         static_cast<const uint8_t *>(rows), slots, weights, static_cast<const uint8_t *>(add), T, k, M, H,
         static_cast<uint8_t *>(out));
-  };
-  if (rows_f32)
-    out_f32 ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
-  else
-    out_f32 ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
+  }, rows_f32, out_f32, whole_lines(out, (long long)H * (out_f32 ? 4 : 2)),
+     read_past_caches((long long)T * k, (long long)H * (rows_f32 ? 4 : 2)));
   return hipGetLastError();
 }
 
@@ -259,15 +282,12 @@ hipError_t launch_combine_rows_grad(const void *dout, bool dout_f32, const void 
                                     const float *weights, int T, int k, int M, int H, void *drows, float *dweights,
                                     hipStream_t s) {
   const int P = T * k, grid = (int)std::min<int64_t>(((int64_t)P + kWaves - 1) / kWaves, kMaxGroups);
-  const auto run = [&](auto r, auto d) {
-    k_combine_rows_grad<decltype(r)::value, decltype(d)::value><<<grid, 64 * kWaves, 0, s>>>(
+  const long long pitch = (long long)H * (rows_f32 ? 4 : 2);
+  with_flags([&](auto r, auto d, auto nt, auto ntl) {
+    k_combine_rows_grad<decltype(r)::value, decltype(d)::value, decltype(nt)::value, decltype(ntl)::value><<<grid, 64 * kWaves, 0, s>>>(
         static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(rows), slots, weights, P, k, M, H,
         static_cast<uint8_t *>(drows), dweights);
-  };
-  if (rows_f32)
-    dout_f32 ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
-  else
-    dout_f32 ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
+  }, rows_f32, dout_f32, whole_lines(drows, pitch), read_past_caches(P, pitch));
   return hipGetLastError();
 }
 

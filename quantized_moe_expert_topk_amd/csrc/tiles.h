@@ -163,8 +163,11 @@ inline int choose_mx(const MxArgs &a, int rows) {
 // default: the stores of wgrad of 8 experts, 264 x 200, made it 7.3 us instead of 5.1.  And rows that begin or end inside
 // a 128-byte line do: their part lines went to memory one by one (wgrad of 60 experts, 1912 x 728: 159 us written
 // through, 33 not; of 256 experts of 128 rows with the output 16 bytes off a line: 1067, 340 not).
+inline bool whole_lines(const void *out, long long pitch) {
+  return pitch % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
+}
 inline bool stores_go_through(const void *out, double bytes, long long pitch) {
-  return bytes > 16e6 && pitch % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
+  return bytes > 16e6 && whole_lines(out, pitch);
 }
 
 }  // namespace qmoe
