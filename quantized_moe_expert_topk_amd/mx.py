@@ -9,10 +9,14 @@ from __future__ import annotations
 import torch
 
 from ._lib import MOE_LAYOUT_ROWS, MOE_LAYOUT_TILE16
-from .grouped import _INT_MAX, _call, _matrix, _operand, _output, _ranges, _rows_hint
-from .rows import _empty, _pairs, _room
+from .grouped import _INT_MAX, _call, _matrix, _output, _ranges, _rows_hint
+from .rows import _BF16, _U8, _arg, _empty, _pairs, _room, _sizes, _values
 
-_U8, _BF16 = (torch.uint8,), (torch.bfloat16,)
+
+def _out(out, out_dtype, shape, device, stream):
+    if out is None or out_dtype is not None:
+        return _output(out, out_dtype, shape, device, stream)
+    return (out, *_values(out, shape, device, "out"))
 
 
 def _width(codes: torch.Tensor, name: str) -> int:
@@ -28,33 +32,33 @@ def moe_quantize_mx(x: torch.Tensor, slots: torch.Tensor | None = None, rows: in
     """bf16 rows [T, K] to codes [M, K / 2] and scales [ceil(K / 128), M, 4].  Without ``slots`` M is T; with slots
     [T, k] token t goes to rows slots[t], the other rows stay as they were, and M is that of ``q`` or ``scale``, else
     ``rows``, else T * k."""
-    T, K = _matrix(x, 2, "x")
+    T, K = _sizes(x, "x")
     dev, G = x.device, (K + 127) // 128
-    px = _operand(x, _BF16, (T, K), dev, "x")
+    px = _arg(x, _BF16, (T, K), dev, "x")
     k, ps, M = 1, None, T
     if slots is not None:
         _, k, ps = _pairs(slots, T, dev)
         if q is not None:
-            M = _matrix(q, 2, "q")[0]
+            M = _sizes(q, "q")[0]
         else:
-            M = _room(rows, None, T, k) if scale is None else _matrix(scale, 3, "scale")[1]
+            M = _room(rows, T, k) if scale is None else _matrix(scale, 3, "scale")[1]
     if q is None:
         q = _empty((M, K // 2), torch.uint8, dev, stream)
     if scale is None:
         scale = _empty((G, M, 4), torch.uint8, dev, stream)
-    _call("moe_quantize_mx", dev, stream, px, ps, T, k, M, K, _operand(q, _U8, (M, K // 2), dev, "q"),
-          _operand(scale, _U8, (G, M, 4), dev, "scale"))
+    _call("moe_quantize_mx", dev, stream, px, ps, T, k, M, K, _arg(q, _U8, (M, K // 2), dev, "q"),
+          _arg(scale, _U8, (G, M, 4), dev, "scale"))
     return q, scale
 
 
 def moe_dequantize_mx(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor | None = None,
                       out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """The values [M, K], bf16 or f32, of quantised rows."""
-    M, _ = _matrix(q, 2, "q")
+    M, _ = _sizes(q, "q")
     K, dev = _width(q, "q"), q.device
-    pq = _operand(q, _U8, (M, K // 2), dev, "q")
-    ps = _operand(scale, _U8, ((K + 127) // 128, M, 4), dev, "scale")
-    out, po, code = _output(out, out_dtype, (M, K), dev, stream)
+    pq = _arg(q, _U8, (M, K // 2), dev, "q")
+    ps = _arg(scale, _U8, ((K + 127) // 128, M, 4), dev, "scale")
+    out, po, code = _out(out, out_dtype, (M, K), dev, stream)
     _call("moe_dequantize_mx", dev, stream, pq, ps, M, K, po, code)
     return out
 
@@ -63,19 +67,19 @@ def _scales(ws: torch.Tensor, layout: int, lead: tuple, N: int, K: int, device) 
     """Scales of E * N weight rows; lead: (E,) or () of a dense product."""
     rows = N * (lead[0] if lead else 1)
     shape = (*lead, N, K // 32) if layout == MOE_LAYOUT_TILE16 else ((K + 127) // 128, rows, 4)
-    return _operand(ws, _U8, shape, device, "ws")
+    return _arg(ws, _U8, shape, device, "ws")
 
 
 def moe_mx_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, layout: int = MOE_LAYOUT_ROWS,
               out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """y = X @ W^T of the values X [M, K] and W [N, K] of two sets of quantised rows -> [M, N] bf16 or f32.  With ``layout``
     MOE_LAYOUT_TILE16, wq [N, K / 2] and ws [N, K / 32] are one matrix of a packed MXFP4 bank."""
-    M, _ = _matrix(xq, 2, "xq")
-    N, _ = _matrix(wq, 2, "wq")
+    M, _ = _sizes(xq, "xq")
+    N, _ = _sizes(wq, "wq")
     K, dev = _width(xq, "xq"), xq.device
-    px, pxs = _operand(xq, _U8, (M, K // 2), dev, "xq"), _operand(xs, _U8, ((K + 127) // 128, M, 4), dev, "xs")
-    pw, pws = _operand(wq, _U8, (N, K // 2), dev, "wq"), _scales(ws, layout, (), N, K, dev)
-    out, po, code = _output(out, out_dtype, (M, N), dev, stream)
+    px, pxs = _arg(xq, _U8, (M, K // 2), dev, "xq"), _arg(xs, _U8, ((K + 127) // 128, M, 4), dev, "xs")
+    pw, pws = _arg(wq, _U8, (N, K // 2), dev, "wq"), _scales(ws, layout, (), N, K, dev)
+    out, po, code = _out(out, out_dtype, (M, N), dev, stream)
     _call("moe_mx_mm", dev, stream, px, pxs, pw, pws, layout, M, N, K, po, code)
     return out
 
@@ -86,13 +90,13 @@ def moe_grouped_mx_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: 
                       out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """:func:`moe_mx_mm` by expert: wq [E, N, K / 2], with ws [ceil(K / 128), E * N, 4] as :func:`moe_quantize_mx` gives it
     for the E * N rows, or [E, N, K / 32] of a packed bank; row ranges as for the grouped products."""
-    M, _ = _matrix(xq, 2, "xq")
+    M, _ = _sizes(xq, "xq")
     E, N, _ = _matrix(wq, 3, "wq")
     K, dev = _width(xq, "xq"), xq.device
-    px, pxs = _operand(xq, _U8, (M, K // 2), dev, "xq"), _operand(xs, _U8, ((K + 127) // 128, M, 4), dev, "xs")
-    pw, pws = _operand(wq, _U8, (E, N, K // 2), dev, "wq"), _scales(ws, layout, (E,), N, K, dev)
+    px, pxs = _arg(xq, _U8, (M, K // 2), dev, "xq"), _arg(xs, _U8, ((K + 127) // 128, M, 4), dev, "xs")
+    pw, pws = _arg(wq, _U8, (E, N, K // 2), dev, "wq"), _scales(ws, layout, (E,), N, K, dev)
     off, cnt = _ranges(offsets, counts, E, dev)
-    out, po, code = _output(out, out_dtype, (M, N), dev, stream)
+    out, po, code = _out(out, out_dtype, (M, N), dev, stream)
     _call("moe_grouped_mx_mm", dev, stream, px, pxs, pw, pws, layout, off, cnt, E, M, _rows_hint(expected_rows, M), N, K,
           po, code)
     return out

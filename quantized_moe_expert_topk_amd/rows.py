@@ -13,13 +13,36 @@ import torch
 from ._streams import allocating_on
 from .grouped import _INT_MAX, _OUT, _call, _matrix, _operand, _output, _ranges
 
-_I32, _F32, _ROWS = (torch.int32,), (torch.float32,), (torch.float32, torch.bfloat16)
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+
+
+# The checks of grouped.py, which a call of a few microseconds spends a good part of its time in: what is right is seen
+# with fewer questions (a cuda device has an index), what is not goes on to those checks, which say what is wrong.
+
+def _arg(t: torch.Tensor, dtype: torch.dtype, shape, device, name: str) -> int:
+    if t.dtype is dtype and t.shape == shape and t.device == device and not t.requires_grad and t.is_contiguous():
+        return t.data_ptr()
+    return _operand(t, (dtype,), shape, device, name)
+
+
+def _sizes(t: torch.Tensor, name: str):
+    """The shape of a matrix on a cuda device."""
+    shape = t.shape
+    if len(shape) == 2 and 0 < t.numel() <= _INT_MAX and t.device.index is not None:
+        return shape
+    return _matrix(t, 2, name)
+
+
+def _values(t: torch.Tensor, shape, device, name: str) -> tuple[int, int]:
+    """(address, type code) of a bf16 or f32 matrix."""
+    dtype = _BF16 if t.dtype is _BF16 else _F32
+    return _arg(t, dtype, shape, device, name), _OUT[dtype]
 
 
 def _pairs(slots: torch.Tensor, T: int | None, device) -> tuple[int, int, int]:
     """(T, k, address) of a slots tensor of T tokens."""
-    shape = _matrix(slots, 2, "slots")
-    p = _operand(slots, _I32, shape if T is None else (T, shape[1]), device, "slots")
+    shape = _sizes(slots, "slots")
+    p = _arg(slots, _I32, shape if T is None else (T, shape[1]), device, "slots")
     return shape[0], shape[1], p
 
 
@@ -32,23 +55,21 @@ def moe_pair_slots(topk_ids: torch.Tensor, sorted_ids: torch.Tensor, offsets: to
                    counts: torch.Tensor | None = None, slots: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The place of every pair in ``sorted_ids``, -1 for a pair that has none.  topk_ids int32 [T, k]; sorted_ids,
     offsets and counts as :func:`moe_align` gives them -> int32 [T, k]."""
-    T, k = _matrix(topk_ids, 2, "topk_ids")
+    T, k = shape = _sizes(topk_ids, "topk_ids")
     dev = topk_ids.device
-    ids = _operand(topk_ids, _I32, (T, k), dev, "topk_ids")
+    ids = _arg(topk_ids, _I32, shape, dev, "topk_ids")
     M, = _matrix(sorted_ids, 1, "sorted_ids")
     E = counts.shape[0] if counts is not None and counts.dim() == 1 else max(offsets.numel() - 1, 0)
     off, cnt = _ranges(offsets, counts, E, dev)
-    at = _operand(sorted_ids, _I32, (M,), dev, "sorted_ids")
+    at = _arg(sorted_ids, _I32, (M,), dev, "sorted_ids")
     if slots is None:
         slots = _empty((T, k), torch.int32, dev, stream)
-    _call("moe_pair_slots", dev, stream, ids, T, k, at, M, off, cnt, E, _operand(slots, _I32, (T, k), dev, "slots"))
+    _call("moe_pair_slots", dev, stream, ids, T, k, at, M, off, cnt, E, _arg(slots, _I32, shape, dev, "slots"))
     return slots
 
 
-def _room(rows: int | None, out: torch.Tensor | None, T: int, k: int) -> int:
-    """Rows of a row matrix that is allocated here, or passed."""
-    if out is not None:
-        return out.shape[0]
+def _room(rows: int | None, T: int, k: int) -> int:
+    """Rows of a row matrix that is allocated here."""
     if rows is None:
         return T * k
     if not 0 <= rows <= _INT_MAX:
@@ -60,19 +81,19 @@ def moe_gather_rows(x: torch.Tensor, slots: torch.Tensor, rows: int | None = Non
                     stream=None) -> torch.Tensor:
     """out[slots[t, j]] = x[t] for every pair.  x [T, H] of any type, rows of whole 16 bytes -> [rows, H] (``rows``: that
     of ``out``, else T * k).  Its gradient for x is :func:`moe_combine_rows` of the rows' gradients, without weights."""
-    T, H = _matrix(x, 2, "x")
+    T, H = shape = _sizes(x, "x")
     dev = x.device
-    px = _operand(x, (x.dtype,), (T, H), dev, "x")
+    px = _arg(x, x.dtype, shape, dev, "x")
     _, k, ps = _pairs(slots, T, dev)
-    if out is not None:
-        _matrix(out, 2, "out")
-    M = _room(rows, out, T, k)
     if out is None:
+        M = _room(rows, T, k)
         out = _empty((M, H), x.dtype, dev, stream)
+    else:
+        M = _sizes(out, "out")[0]
     width = H * x.element_size()
     if width > _INT_MAX:
         raise ValueError(f"x: rows of {width} bytes are too large for 32-bit sizes")
-    _call("moe_gather_rows", dev, stream, px, T, k, ps, width, M, _operand(out, (x.dtype,), (M, H), dev, "out"))
+    _call("moe_gather_rows", dev, stream, px, T, k, ps, width, M, _arg(out, x.dtype, (M, H), dev, "out"))
     return out
 
 
@@ -81,14 +102,17 @@ def moe_combine_rows(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Ten
                      out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """out[t] = add[t] + sum_j weights[t, j] * rows[slots[t, j]].  rows [M, H] bf16 or f32, weights f32 [T, k] (None:
     ones), add [T, H] of out's type -> [T, H] of ``out_dtype`` (rows' type if None)."""
-    M, H = _matrix(rows, 2, "rows")
+    M, H = shape = _sizes(rows, "rows")
     dev = rows.device
-    pr = _operand(rows, _ROWS, (M, H), dev, "rows")
+    pr, rt = _values(rows, shape, dev, "rows")
     T, k, ps = _pairs(slots, None, dev)
-    pw = _operand(weights, _F32, (T, k), dev, "weights") if weights is not None else None
-    out, po, code = _output(out, out_dtype or (rows.dtype if out is None else None), (T, H), dev, stream)
-    pa = _operand(add, (out.dtype,), (T, H), dev, "add") if add is not None else None
-    _call("moe_combine_rows", dev, stream, pr, _OUT[rows.dtype], ps, pw, pa, T, k, M, H, po, code)
+    pw = _arg(weights, _F32, (T, k), dev, "weights") if weights is not None else None
+    if out is None or out_dtype is not None:
+        out, po, code = _output(out, out_dtype or rows.dtype, (T, H), dev, stream)
+    else:
+        po, code = _values(out, (T, H), dev, "out")
+    pa = _arg(add, out.dtype, (T, H), dev, "add") if add is not None else None
+    _call("moe_combine_rows", dev, stream, pr, rt, ps, pw, pa, T, k, M, H, po, code)
     return out
 
 
@@ -96,17 +120,17 @@ def moe_combine_rows_grad(dout: torch.Tensor, rows: torch.Tensor, slots: torch.T
                           drows: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
     """The gradients of :func:`moe_combine_rows` with weights: drows[slots[t, j]] = weights[t, j] * dout[t] (of rows' shape
     and type) and dweights[t, j] = <rows[slots[t, j]], dout[t]> (f32 [T, k], 0 for pairs without a row)."""
-    T, H = _matrix(dout, 2, "dout")
-    M, _ = _matrix(rows, 2, "rows")
-    dev = dout.device
-    pd = _operand(dout, _ROWS, (T, H), dev, "dout")
-    pr = _operand(rows, _ROWS, (M, H), dev, "rows")
+    T, H = _sizes(dout, "dout")
+    M = _sizes(rows, "rows")[0]
+    dev, shape = dout.device, (M, H)
+    pd, dt = _values(dout, (T, H), dev, "dout")
+    pr, rt = _values(rows, shape, dev, "rows")
     _, k, ps = _pairs(slots, T, dev)
-    pw = _operand(weights, _F32, (T, k), dev, "weights")
+    pw = _arg(weights, _F32, (T, k), dev, "weights")
     if drows is None:
-        drows = _empty((M, H), rows.dtype, dev, stream)
+        drows = _empty(shape, rows.dtype, dev, stream)
     if dweights is None:
-        dweights = _empty((T, k), torch.float32, dev, stream)
-    _call("moe_combine_rows_grad", dev, stream, pd, _OUT[dout.dtype], pr, _OUT[rows.dtype], ps, pw, T, k, M, H,
-          _operand(drows, (rows.dtype,), (M, H), dev, "drows"), _operand(dweights, _F32, (T, k), dev, "dweights"))
+        dweights = _empty((T, k), _F32, dev, stream)
+    _call("moe_combine_rows_grad", dev, stream, pd, dt, pr, rt, ps, pw, T, k, M, H,
+          _arg(drows, rows.dtype, shape, dev, "drows"), _arg(dweights, _F32, (T, k), dev, "dweights"))
     return drows, dweights
