@@ -281,7 +281,9 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
   // D register j of a lane: i = 8 (j / 4) + 4 h + j % 4 of fragment p, row lane % 32 of q.  i of fragment p is column 32 p + i
   // of the wave's, or TP i + p (packed).  Lanes trade pieces of 16 bytes, so that four of them hold 64 consecutive bytes of
   // a row: a wave issues exactly STORES stores of 16 bytes a lane where rows are whole such pieces (N a multiple of 8, or
-  // of 4 in fp32), whatever part of the tile exists (the resource refuses the rest).
+  // of 4 in fp32), whatever part of the tile exists (the resource refuses the rest).  Other rows take the same pieces where
+  // they lie, unaligned, and the last one element by element (60 experts, 5000 x 1001 x 1440: single elements 36 us, so
+  // ODD_US; 1000 columns 19).
   auto store = [&]() __attribute__((always_inline)) {
     constexpr uint32_t OS = OUT_BF16 ? 2 : 4;
     constexpr int PIECE = 16 / OS;
@@ -309,7 +311,23 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
     };
     const auto put = [&](auto policy) __attribute__((always_inline)) {
       const auto store16 = [&](const u32x4 &v, int row, int c) __attribute__((always_inline)) {
-        __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)(c < a.N ? row * out_pitch + c * OS : kNowhere), 0, policy());
+        if constexpr (policy() >= 0) {
+          __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)(c < a.N ? row * out_pitch + c * OS : kNowhere), 0, policy());
+        } else if (row < o.rows && c < a.N) {
+          uint8_t *at = static_cast<uint8_t *>(a.out) + (size_t)(o.q0 + row) * out_pitch + (size_t)c * OS;
+          if (c + PIECE <= a.N) {
+            __builtin_memcpy(at, &v, 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PIECE - 1; i++)
+              if (c + i < a.N) {
+                if constexpr (OUT_BF16)
+                  reinterpret_cast<uint16_t *>(at)[i] = (uint16_t)(v[i / 2] >> 16 * (i % 2));
+                else
+                  reinterpret_cast<uint32_t *>(at)[i] = v[i];
+              }
+          }
+        }
       };
 #pragma unroll
       for (int q = 0; q < TQ; q++) {
@@ -381,28 +399,14 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
         }
       }
     };
-    if (a.N % (OUT_BF16 ? 8 : 4) == 0) {
+    if (a.N % PIECE != 0) {
+      put(std::integral_constant<int, -1>{});
+    } else {
       if (a.write_through)
         put(std::integral_constant<int, kWriteThrough>{});
       else
         put(std::integral_constant<int, 0>{});
       stored = 1;
-      return;
-    }
-#pragma unroll
-    for (int q = 0; q < TQ; q++) {
-      const uint32_t row = ((wq * TQ + q) * 32 + r32) * out_pitch;
-#pragma unroll
-      for (int p = 0; p < TP; p++)
-#pragma unroll
-        for (int j = 0; j < 16; j++) {
-          const int i = 8 * (j / 4) + 4 * h + j % 4, c = c0 + (MIXED ? TP * i + p : p * 32 + i);
-          const int off = (int)(c < a.N ? row + c * OS : kNowhere);
-          if constexpr (OUT_BF16)
-            __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(acc[p][q][j]), ro, off, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[p][q][j]), ro, off, 0, 0);
-        }
     }
   };
 
