@@ -107,7 +107,7 @@ __device__ __forceinline__ int add_tiles(int a, int b) { return min(a + b, kMany
 
 template <int THREADS>
 __device__ __forceinline__ int make_tile_table(const Groups &g, int BM, int32_t *first) {
-  constexpr int EPT = kMaxExperts / THREADS, W = THREADS / 64;
+  constexpr int EPT = (kMaxExperts + THREADS - 1) / THREADS, W = THREADS / 64;
   __shared__ int32_t totals[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int tiles[EPT], sum = 0;

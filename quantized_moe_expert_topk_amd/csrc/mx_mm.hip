@@ -2,9 +2,22 @@
 //
 //   y[r, n] = sum_b 2^(xs[r, b] + ws[n, b] - 254) sum_{k in block b} xq[r, k] wq[n, k]
 //
-// The pipeline of product_dev.h (persistent workgroups, operands loaded straight to LDS NS stages ahead across the tiles'
-// borders, fragments read one step ahead of the products), with p along n and q along the rows.  A stage is 128 bytes of
-// each row, 256 columns, and their scales.
+// D[p, q] = sum_c A[p, c] B[q, c] with p along n and q along the rows, as product_dev.h does it: persistent workgroups that
+// take tiles in an order their XCD shares, operands loaded straight to LDS NS stages ahead across the tiles' borders,
+// fragments read one step ahead of the products.  A stage is 128 bytes of each row, 256 columns, and their scales.
+//
+// What bounds it.  8192 x 4096 x 4096, bf16 (us, parts left out in turn): all 71; without stores 63; loads alone 37, matrix
+// instructions and their LDS reads alone 37, the two without LDS reads 49: the clock falls with what the matrix cores spend
+// (operands held in registers reach 6.6 PFLOP/s, 42 us), and loads into LDS and reads from it share its port.  65536 rows of
+// 256 experts, 1024 x 2048 (490 MB): 129; loads alone 83, of one tile only 55, without stores 100: memory, then the stores.
+// Choices, with what they measured at 8192 x 4096 x 4096 unless another size is given:
+// - 32 x 32 x 64 instructions (mx_dev.h), a wave tile of 64 x 64: most products a byte read from LDS that leaves room for
+//   three stages; 256 x 256 tiles with two stages took as long (72, and 176 against 165 for 8 experts of 2048 rows).
+// - Four waves that only load beside eight that multiply (APART), for 256 x 128 tiles: 76 to 72, 8 experts of 2048 rows 184 to
+//   165.  Smaller tiles are bound by memory's latency, and load in the waves that multiply (1000 rows: 14 for 18).
+// - Products pinned to their step (pin()): 92 to 81; loads beside all of a stage's steps: 81 to 77.
+// - Packed weights lie in LDS as in memory: 1 KB contiguous a load (prefill above 164 to 150), scales of a wave's two
+//   fragments in one operand (140 to 133).
 #include <algorithm>
 #include <iterator>
 #include <type_traits>
@@ -47,15 +60,16 @@ struct MxTile {
   int e, p0, q0, rows;  // rows: output rows q0, q0 + 1, ... that exist
 };
 
-template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool TILE16, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
-  constexpr int W = WP * WQ, THREADS = 64 * W, TP = BP / WP / 32, TQ = BQ / WQ / 32;
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool APART, bool TILE16, bool OUT_BF16>
+__global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) void k_mx_product(MxArgs a) {
+  // APART: the first four waves load, and the others multiply; else every wave does both.
+  constexpr int W = APART ? 4 : WP * WQ, THREADS = 64 * W, TP = BP / WP / 32, TQ = BQ / WQ / 32;  // W: waves that load
   using ATile = std::conditional_t<TILE16, PackedTile<BP, THREADS, TP>, RowTile<BP, THREADS>>;
   using BTile = RowTile<BQ, THREADS>;
   // Scales in LDS, a dword for each row: of the weights' first group of 128 columns, of their second, then of x.  A dword is
   // four blocks of a row; of a packed bank's weights, one block of four rows, 16 rows x 4 blocks after one another.  Four
-  // waves load a group each, 16 bytes a lane (a load to LDS takes its 20 cycles of the CU whatever it brings: with 4 bytes
-  // a lane, 16 of them a stage, 8192 x 4096 x 4096 took 71 us).
+  // waves load a group each, 16 bytes a lane: a load to LDS takes some 20 cycles of the CU whatever it brings (4 bytes a
+  // lane, 16 loads a stage instead of 4: 8 us more at 8192 x 4096 x 4096).
   constexpr int CODES = ATile::kBytes + BTile::kBytes, STAGE = CODES + (BP + BQ) * 8;
   constexpr int LOADS = ATile::NL + BTile::NL + 1;  // per thread and stage
   static_assert(W >= 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
@@ -63,12 +77,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
   __shared__ int32_t first[kMaxExperts + 1];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wp = wave % WP, wq = wave / WP, h = lane >> 5, r32 = lane & 31;
+  const int mul = APART ? wave - 4 : wave, wp = mul % WP, wq = mul / WP, h = lane >> 5, r32 = lane & 31;
   const int units = a.K / 32;
   const uint32_t pitch = (uint32_t)units * 16;
 
   int q_total = (a.g.M + BQ - 1) / BQ;
-  if (a.g.offsets) q_total = make_tile_table<THREADS>(a.g, BQ, first);
+  if (a.g.offsets) q_total = make_tile_table<THREADS + (APART ? 64 * WP * WQ : 0)>(a.g, BQ, first);
 
   // The tiles' order and the XCDs' shares of it are those of k_product.  (A quotient is computed in vector registers; what
   // comes of it has to be scalar again, for the loads' resources.)
@@ -170,8 +184,39 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
   MxTile o;
   int ct = lt;
   if (!locate(ct, o)) return;
+  const int n_stages = (units + KB / 16 - 1) / (KB / 16);
+  if constexpr (APART) {
+    if (wave < 4) {
+      // The waves meet once a stage (and once before the first): the next stage has been loaded, this one's slot read.
+      lt = ct;
+      start(o);
+#pragma unroll
+      for (int s = 0; s < NS; s++) {
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) load(s, i);
+        close();
+      }
+      wait_vm<(NS - 1) * LOADS>();
+      barrier_only();
+      int slot = 0;
+      for (;;) {
+        for (int s = 0; s < n_stages; s++) {
+          wait_vm<(NS - 2) * LOADS>();
+          barrier_only();
+#pragma unroll
+          for (int i = 0; i < LOADS; i++) load(slot, i);
+          close();
+          slot = slot == NS - 1 ? 0 : slot + 1;
+        }
+        ct += gridDim.x;
+        if (!locate(ct, o)) break;
+      }
+      wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
+      return;
+    }
+  }
   lt = ct;
-  start(o);
+  if constexpr (!APART) start(o);
   f32x16_t acc[TP][TQ];
   // Step ks multiplies the units ks (lanes 0..31) and 4 + ks (lanes 32..63) of a stage: the scales of a lane's four steps are
   // then the bytes of one dword, which the instruction picks from (packed banks: those of the fragments).
@@ -237,7 +282,8 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
       for (int p = 0; p < TP; p++) sa[0][p] = sa[1][p];
     }
   };
-  // Products may not move past this point: without it they sink behind the next barrier, and the matrix core idles until it.
+  // Products may not move past this point: the compiler would sink them behind the next barrier, and the matrix core idle
+  // until it.
   auto pin = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < TP; p++)
@@ -250,7 +296,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
       constexpr bool last = ks == NKS - 1;
       constexpr int cur = ks & 1;
       if constexpr (last) {
-        wait_loads();
+        if constexpr (!APART) wait_loads();
         barrier_only();
         fill = slot;
         read_scales(next);
@@ -268,11 +314,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
         constexpr int SPAN = NS > 2 ? NKS : 1, at = (ks + 1) % NKS * TICKS + i;  // ticks from the meeting on
         constexpr int j0 = at >= SPAN * TICKS ? LOADS : at * LOADS / (SPAN * TICKS);
         constexpr int j1 = at >= SPAN * TICKS ? LOADS : (at + 1) * LOADS / (SPAN * TICKS);
-        static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(fill, j0 + j); });
+        if constexpr (!APART)
+          static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(fill, j0 + j); });
         __builtin_amdgcn_sched_barrier(0);
       });
       pin();
-      if constexpr (ks == (NS > 2 ? NKS - 2 : NKS - 1)) close();
+      if constexpr (!APART && ks == (NS > 2 ? NKS - 2 : NKS - 1)) close();
       if constexpr (last) use_scales();
     });
     slot = next;
@@ -283,7 +330,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
   // a row: a wave issues exactly STORES stores of 16 bytes a lane where rows are whole such pieces (N a multiple of 8, or
   // of 4 in fp32), whatever part of the tile exists (the resource refuses the rest).  Other rows take the same pieces where
   // they lie, unaligned, and the last one element by element (60 experts, 5000 x 1001 x 1440: single elements 36 us, so
-  // ODD_US; 1000 columns 19).
+  // 22; 1000 columns 19).
   auto store = [&]() __attribute__((always_inline)) {
     constexpr uint32_t OS = OUT_BF16 ? 2 : 4;
     constexpr int PIECE = 16 / OS;
@@ -410,19 +457,20 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
     }
   };
 
+  if constexpr (!APART) {
 #pragma unroll
-  for (int s = 0; s < NS; s++) {
+    for (int s = 0; s < NS; s++) {
 #pragma unroll
-    for (int i = 0; i < (s < NS - 1 ? LOADS : FIRST); i++) load(s, i);
-    if (s < NS - 1 || FIRST == LOADS) close();
+      for (int i = 0; i < (s < NS - 1 ? LOADS : FIRST); i++) load(s, i);
+      if (s < NS - 1 || FIRST == LOADS) close();
+    }
+    wait_vm<(NS - 2) * LOADS + FIRST>();
   }
-  wait_vm<(NS - 2) * LOADS + FIRST>();
   barrier_only();
 #pragma unroll
   for (int i = 0; i < NR; i++) read(0, 0, 0, i);
   read_scales(0);
   use_scales();
-  const int n_stages = (units + KB / 16 - 1) / (KB / 16);
   for (;;) {
 #pragma unroll
     for (int p = 0; p < TP; p++)
@@ -435,12 +483,12 @@ __global__ __launch_bounds__(64 * WP * WQ, 2) void k_mx_product(MxArgs a) {
     ct += gridDim.x;
     if (!locate(ct, o)) break;
   }
-  wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
+  if constexpr (!APART) wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
 }
 
 namespace {
 
-template <int BP, int BQ, int WP, int WQ, int NS, bool NT>
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool APART>
 hipError_t run_mx(MxArgs a, bool out_bf16, hipStream_t s) {
   a.p_tiles = (a.N + BP - 1) / BP;
   const long long q = a.g.offsets ? a.g.M / BQ + std::min(a.g.E, a.g.M) : (a.g.M + BQ - 1) / BQ;  // the most there can be
@@ -453,7 +501,8 @@ hipError_t run_mx(MxArgs a, bool out_bf16, hipStream_t s) {
   constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 2 : 1);
   const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
   const auto run = [&](auto packed, auto bf16) {
-    k_mx_product<BP, BQ, WP, WQ, NS, NT, decltype(packed)::value, decltype(bf16)::value><<<grid, 64 * WP * WQ, 0, s>>>(a);
+    k_mx_product<BP, BQ, WP, WQ, NS, NT, APART, decltype(packed)::value, decltype(bf16)::value>
+        <<<grid, 64 * (WP * WQ + (APART ? 4 : 0)), 0, s>>>(a);
   };
   if (a.tile16)
     out_bf16 ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
@@ -469,7 +518,7 @@ template <size_t... I>
 static hipError_t run_mx_tile(int t, const MxArgs &a, bool out_bf16, hipStream_t s, std::index_sequence<I...>) {
   hipError_t e = hipErrorInvalidValue;
   (void)((t == (int)I && (e = run_mx<kMxTiles[I].bp, kMxTiles[I].bq, kMxTiles[I].wp, kMxTiles[I].wq, kMxTiles[I].stages,
-                                     kMxTiles[I].nt>(a, out_bf16, s), true)) || ...);
+                                     kMxTiles[I].nt, kMxTiles[I].apart>(a, out_bf16, s), true)) || ...);
   return e;
 }
 

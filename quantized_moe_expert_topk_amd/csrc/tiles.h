@@ -9,10 +9,11 @@
 
 namespace qmoe {
 
-// k_product's parameters: outputs a workgroup, waves along p and q, stages in LDS, weights non-temporal.
+// k_product's parameters: outputs a workgroup, waves along p and q, stages in LDS, weights non-temporal.  k_mx_product's
+// too, with whether waves of their own load.
 struct Tile {
   int bp, bq, wp, wq, stages;
-  bool nt;
+  bool nt, apart = false;
 };
 
 // The tiles that each product is built for; the choices below are places in these.
@@ -125,25 +126,25 @@ inline int choose_block(const ProductArgs &a, int rows) {
 
 // The MXFP4 products: k_mx_product's tiles (mx_mm.hip), or k_mx_few (mx_few.hip).
 inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true},   {128, 64, 4, 2, 5, true},   {128, 128, 2, 4, 4, false},
-                                    {256, 128, 4, 2, 3, false}, {256, 128, 4, 2, 3, true}, {256, 256, 2, 4, 2, false}};
+                                    {256, 128, 4, 2, 3, false, true}, {256, 128, 4, 2, 3, true, true}};
 
 // Measured (MI355X, us).  k_mx_few costs 4.5 us and moves 3.9 bytes of weights a ns, once per 16 rows; 128 x 32 tiles, one
 // for each CU at most, 5 us and 0.22 a stage: 16 x 4096 x 4096 7.3 / 8.3, 64 rows 12.2 / 8.5, one row of 8 of 256 experts,
-// 1024 x 2048, 8.3 / 10.9.  Then the smallest tiles that one round over the CUs holds, whose stages take the least time:
-//                            128 x 32   128 x 64   128 x 128   256 x 128   256 x 256
-//   256 x 4096 x 4096           11.2       11.3       11.9        15.7        25.7
-//   512 x 4096 x 4096           17.9       12.4       12.5        16.4        26.7
-//   1000 x 4096 x 4096          31.4       21.0       14.1        18.0        26.8
-//   2000 x 4096 x 4096          57.5       39.3       23.4        21.0        27.5
-// and for large groups the fewest bytes per product (8192 x 4096 x 4096: 256 x 128 75, 256 x 256 71; 8 experts of 2048 rows,
-// 4096 x 4096, packed: 181, 176).  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is to read;
-// non-temporal where the mean is two row tiles at most (nt), unless rows end inside lines, which such loads fetch again
-// (60 experts, 5000 x 1001 x 1440: 36 without, 42 with):
+// 1024 x 2048, 8.1 / 10.9.  Then the smallest tiles that one round over the CUs holds, whose stages take the least time:
+//                            128 x 32   128 x 64   128 x 128   256 x 128
+//   256 x 4096 x 4096           11.2       11.3       11.9
+//   512 x 4096 x 4096           17.9       12.4       12.5        16.4
+//   1000 x 4096 x 4096          31.4       21.0       14.1        16.4
+//   2000 x 4096 x 4096          57.5       39.3       23.4        21.3
+// and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
+// to read; non-temporal where the mean is two row tiles at most (nt; 8192 x 4096 x 4096 72 without, 87 with), unless rows end
+// inside lines, which such loads fetch again (60 experts, 5000 x 1001 x 1440: 22 without, 28 with):
 //             128 x 32   128 x 64   256 x 128   256 x 128 nt
 //   m = 8        49.6       50.1       56.3         51.4
-//   m = 24       59.4       57.3       60.5         54.5
-//   m = 100     133.5       99.9       79.4         76.2
-//   m = 256, +- 260        201.6      135.0        130.1
+//   m = 24       59.4       57.3       60.1         54.9
+//   m = 48       86.9       64.0       68.5         63.7
+//   m = 100     133.5       99.9       83.7         81.2
+//   m = 256, +- 260        201.6      133.1        130.8
 inline int choose_mx(const MxArgs &a, int rows) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
   const auto q_tiles = [&](int bq) { return a.g.offsets ? (long long)rows / bq + std::min(a.g.E, rows) : ((long long)rows + bq - 1) / bq; };  // about
@@ -153,7 +154,6 @@ inline int choose_mx(const MxArgs &a, int rows) {
   if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return 0;
   if (tiles(128, 64) <= 256) return 1;
   if (tiles(128, 128) <= 256) return 2;
-  if (mean > 512 && tiles(256, 256) > 256) return 5;
   return a.g.offsets && mean <= 256 && (a.tile16 || a.K % 256 == 0) ? 4 : 3;
 }
 
