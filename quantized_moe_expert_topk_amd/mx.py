@@ -9,8 +9,8 @@ from __future__ import annotations
 import torch
 
 from ._lib import MOE_LAYOUT_ROWS, MOE_LAYOUT_TILE16
-from .grouped import _INT_MAX, _call, _matrix, _output, _ranges, _rows_hint
-from .rows import _BF16, _U8, _arg, _empty, _pairs, _room, _sizes, _values
+from .grouped import _INT_MAX, _call, _matrix, _output, _rows_hint
+from .rows import _BF16, _U8, _arg, _empty, _pairs, _room, _runs, _sizes, _values
 
 
 def _out(out, out_dtype, shape, device, stream):
@@ -95,7 +95,7 @@ def moe_grouped_mx_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: 
     K, dev = _width(xq, "xq"), xq.device
     px, pxs = _arg(xq, _U8, (M, K // 2), dev, "xq"), _arg(xs, _U8, ((K + 127) // 128, M, 4), dev, "xs")
     pw, pws = _arg(wq, _U8, (E, N, K // 2), dev, "wq"), _scales(ws, layout, (E,), N, K, dev)
-    off, cnt = _ranges(offsets, counts, E, dev)
+    off, cnt = _runs(offsets, counts, E, dev)
     out, po, code = _out(out, out_dtype, (M, N), dev, stream)
     _call("moe_grouped_mx_mm", dev, stream, px, pxs, pw, pws, layout, off, cnt, E, M, _rows_hint(expected_rows, M), N, K,
           po, code)

@@ -39,6 +39,14 @@ def _values(t: torch.Tensor, shape, device, name: str) -> tuple[int, int]:
     return _arg(t, dtype, shape, device, name), _OUT[dtype]
 
 
+def _runs(offsets: torch.Tensor, counts: torch.Tensor | None, E: int, device):
+    """The addresses of the row ranges of E experts."""
+    if offsets.dtype is _I32 and offsets.device == device and offsets.dim() == 1 and offsets.is_contiguous() \
+            and offsets.shape[0] >= E + (counts is None):
+        return offsets.data_ptr(), None if counts is None else _arg(counts, _I32, (E,), device, "counts")
+    return _ranges(offsets, counts, E, device)
+
+
 def _pairs(slots: torch.Tensor, T: int | None, device) -> tuple[int, int, int]:
     """(T, k, address) of a slots tensor of T tokens."""
     shape = _sizes(slots, "slots")
@@ -60,7 +68,7 @@ def moe_pair_slots(topk_ids: torch.Tensor, sorted_ids: torch.Tensor, offsets: to
     ids = _arg(topk_ids, _I32, shape, dev, "topk_ids")
     M, = _matrix(sorted_ids, 1, "sorted_ids")
     E = counts.shape[0] if counts is not None and counts.dim() == 1 else max(offsets.numel() - 1, 0)
-    off, cnt = _ranges(offsets, counts, E, dev)
+    off, cnt = _runs(offsets, counts, E, dev)
     at = _arg(sorted_ids, _I32, (M,), dev, "sorted_ids")
     if slots is None:
         slots = _empty((T, k), torch.int32, dev, stream)
