@@ -436,8 +436,8 @@ int moe_grouped_block_mm(const void *xq, const float *xs, const void *wq, const 
  * rows back to the tokens with their routing weights, each with its gradient.  f = t*k + j is token t's j-th pair.
  *   slots        [T, k] int32 device array: the row of pair f in the row matrices (moe_pair_slots makes it), or a
  *                value outside [0, M) where the pair has none.  No value makes a call read or write outside its
- *                matrices.  Rows that two pairs share are read for both; written by both (moe_gather_rows and
- *                moe_combine_rows_grad) they hold one or the other.
+ *                matrices.  Rows that two pairs share are read for both; where both write them
+ *                (moe_gather_rows, moe_combine_rows_grad, moe_quantize_mx) what they hold is undefined.
  *   M            rows of the row matrices.  Rows of no pair are neither read nor written.
  * Sums are fp32 in a fixed order: results do not vary from call to call.  No call needs a workspace.
  * Requires T*k < 2^31 - 1024, H a multiple of 8 and at most 2 million, and 16-byte aligned matrices; an output must
