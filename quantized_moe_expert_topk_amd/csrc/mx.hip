@@ -21,7 +21,6 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-
 }  // namespace
 
 // slots NULL: row t of x is row t of q (k is 1).  Else a token is quantised once and written to each of its rows.

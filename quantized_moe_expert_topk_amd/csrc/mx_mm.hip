@@ -73,6 +73,7 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
   constexpr int CODES = ATile::kBytes + BTile::kBytes, STAGE = CODES + (BP + BQ) * 8;
   constexpr int LOADS = ATile::NL + BTile::NL + 1;  // per thread and stage
   static_assert(W >= 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
+  static_assert(NS > 2 && TP <= 2, "a stage of time between a load and its use; scales of two fragments together");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   __shared__ int32_t first[kMaxExperts + 1];
 
@@ -238,9 +239,8 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
   uint4 af[2][TP], bf[2][TQ];
   uint32_t sa[2][TILE16 ? 1 : TP], sb[TQ], sb_next[TQ];  // sa: of a step (packed banks), or of this stage and the next one
   // Before a stage's last step the waves meet: its slot has been read, and the next one is loaded.  The slot's loads then go
-  // out beside the four steps up to the next meeting, the first FIRST of them beside the first; with two slots, which leave
-  // one stage of time, all of them.
-  constexpr int FIRST = NS > 2 ? LOADS / NKS : LOADS;
+  // out beside the four steps up to the next meeting, the first FIRST of them beside the first.
+  constexpr int FIRST = LOADS / NKS;
   int slot = 0, fill = NS - 1, stored = 0;
   constexpr int STORES = TP * TQ * (OUT_BF16 ? 2 : 4);
   auto wait_loads = [&]() __attribute__((always_inline)) {
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
       if constexpr (TILE16) {
         af[to][p] = *reinterpret_cast<const uint4 *>(t + a_at[p] + ks * 256);
         const uint8_t *s = t + sa_at + ks * 16;
-        if (p == 0) sa[to][0] = TP == 4 ? *reinterpret_cast<const uint32_t *>(s) : TP == 2 ? *reinterpret_cast<const uint16_t *>(s) : *s;
+        if (p == 0) sa[to][0] = TP == 2 ? *reinterpret_cast<const uint16_t *>(s) : *s;
       } else {
         af[to][p] = *reinterpret_cast<const uint4 *>(t + a_at[ks] + p * 32 * KB);
       }
@@ -311,15 +311,15 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
         static_for<r1 - r0>([&](auto r) __attribute__((always_inline)) {
           read(last ? next : slot, last ? 0 : ks + 1, cur ^ 1, r0 + r);
         });
-        constexpr int SPAN = NS > 2 ? NKS : 1, at = (ks + 1) % NKS * TICKS + i;  // ticks from the meeting on
-        constexpr int j0 = at >= SPAN * TICKS ? LOADS : at * LOADS / (SPAN * TICKS);
-        constexpr int j1 = at >= SPAN * TICKS ? LOADS : (at + 1) * LOADS / (SPAN * TICKS);
-        if constexpr (!APART)
+        if constexpr (!APART) {
+          constexpr int at = (ks + 1) % NKS * TICKS + i;  // ticks from the meeting on
+          constexpr int j0 = at * LOADS / (NKS * TICKS), j1 = (at + 1) * LOADS / (NKS * TICKS);
           static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(fill, j0 + j); });
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
       pin();
-      if constexpr (!APART && ks == (NS > 2 ? NKS - 2 : NKS - 1)) close();
+      if constexpr (!APART && ks == NKS - 2) close();
       if constexpr (last) use_scales();
     });
     slot = next;
@@ -339,19 +339,11 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
     const rsrc_t ro = make_rsrc(static_cast<uint8_t *>(a.out) + (size_t)o.q0 * out_pitch, o.rows * out_pitch);
     const int c0 = o.p0 + wp * TP * 32, s = lane >> 4 & 1, r16 = lane & 15;
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    // what a lane and the one 16 (32) lanes away hold of x and y, so that the first ends with both x, the second with both y
+    // what a lane and the one 16 lanes away hold of x and y, so that the first ends with both x, the second with both y
     const auto trade16 = [](u32x4 &x, u32x4 &y) __attribute__((always_inline)) {
 #pragma unroll
       for (int w = 0; w < 4; w++) {
         const auto v = __builtin_amdgcn_permlane16_swap(x[w], y[w], false, false);
-        x[w] = v[0];
-        y[w] = v[1];
-      }
-    };
-    const auto trade32 = [](u32x4 &x, u32x4 &y) __attribute__((always_inline)) {
-#pragma unroll
-      for (int w = 0; w < 4; w++) {
-        const auto v = __builtin_amdgcn_permlane32_swap(x[w], y[w], false, false);
         x[w] = v[0];
         y[w] = v[1];
       }
@@ -418,7 +410,8 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
             store16(x, row, c);
             store16(y, row + 16, c);
           }
-        } else if constexpr (RUN == 2 * PIECE) {
+        } else {
+          static_assert(RUN == 2 * PIECE, "runs of half a piece, one or two");
 #pragma unroll
           for (int n = 0; n < TP * 16 / PIECE; n += 2) {
             u32x4 x = piece(n), y = piece(n + 1);
@@ -426,22 +419,6 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
             const int c = c0 + 2 * RUN * (n / 2) + RUN * h + PIECE * s;
             store16(x, row, c);
             store16(y, row + 16, c);
-          }
-        } else {
-          static_assert(RUN * OS <= 16 || RUN <= 4 * PIECE, "runs of at most four pieces");
-#pragma unroll
-          for (int n = 0; n < TP * 16 / PIECE; n += 4) {
-            u32x4 x[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) x[i] = piece(n + i);
-            trade16(x[0], x[1]);
-            trade16(x[2], x[3]);
-            trade32(x[0], x[2]);
-            trade32(x[1], x[3]);
-            // x[i]: piece 2 h + s of the lane that has row 16 (i % 2) and run 2 (n / 4) + i / 2
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              store16(x[i], row + 16 * (i % 2), c0 + RUN * (2 * (n / 4) + i / 2) + PIECE * (2 * h + s));
           }
         }
       }
@@ -462,7 +439,7 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
     for (int s = 0; s < NS; s++) {
 #pragma unroll
       for (int i = 0; i < (s < NS - 1 ? LOADS : FIRST); i++) load(s, i);
-      if (s < NS - 1 || FIRST == LOADS) close();
+      if (s < NS - 1) close();
     }
     wait_vm<(NS - 2) * LOADS + FIRST>();
   }

@@ -251,7 +251,8 @@ static void with_flags(F &&f, bool b, B... more) {
 
 // Pair rows are read non-temporally where they are more than the last cache keeps for the kernel after the one that wrote
 // them (256 MB, outputs and weights besides).  Combine, us without / with: 268 MB 66 / 55, 201 MB 49 / 42, 131 MB 34 / 31,
-// but 67 MB that are still in that cache 18 / 20.
+// but 67 MB that are still in that cache 18 / 20.  (The gradients only where rows are whole lines: 268 MB 115 / 108, but 131 MB
+// of 2000-byte rows 63 / 66.)
 static bool read_past_caches(long long rows, long long pitch) { return rows * pitch > 100'000'000; }
 
 hipError_t launch_gather_rows(const void *x, int T, int k, const int32_t *slots, int M, void *rows, int row_bytes,
@@ -287,7 +288,7 @@ hipError_t launch_combine_rows_grad(const void *dout, bool dout_f32, const void 
     k_combine_rows_grad<decltype(r)::value, decltype(d)::value, decltype(nt)::value, decltype(ntl)::value><<<grid, 64 * kWaves, 0, s>>>(
         static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(rows), slots, weights, P, k, M, H,
         static_cast<uint8_t *>(drows), dweights);
-  }, rows_f32, dout_f32, whole_lines(drows, pitch), read_past_caches(P, pitch));
+  }, rows_f32, dout_f32, whole_lines(drows, pitch), whole_lines(rows, pitch) && read_past_caches(P, pitch));
   return hipGetLastError();
 }
 

@@ -36,7 +36,10 @@ def moe_quantize_mx(x: torch.Tensor, slots: torch.Tensor | None = None, rows: in
     dev, G = x.device, (K + 127) // 128
     px = _arg(x, _BF16, (T, K), dev, "x")
     k, ps, M = 1, None, T
-    if slots is not None:
+    if slots is None:
+        if rows is not None and rows != T:
+            raise ValueError(f"rows: without slots the {T} rows of x are quantised, not {rows}")
+    else:
         _, k, ps = _pairs(slots, T, dev)
         if q is not None:
             M = _sizes(q, "q")[0]

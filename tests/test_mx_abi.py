@@ -105,6 +105,7 @@ BAD = [
     (lambda: qm.moe_quantize_mx(bf(4, 64), q=u8(4, 32), scale=u8(4, 2)), "scale"),
     (lambda: qm.moe_quantize_mx(bf(4, 64), ints(4, 2), q=u8(9, 32), scale=u8(1, 8, 4)), "scale"),
     (lambda: qm.moe_quantize_mx(bf(4, 64), ints(4, 2), rows=-1), "rows"),
+    (lambda: qm.moe_quantize_mx(bf(4, 64), rows=8), "rows"),
     (lambda: qm.moe_dequantize_mx(u8(*Q), u8(64, 5), out=bf(64, 160)), "scale"),
     (lambda: qm.moe_dequantize_mx(u8(*Q), u8(*S), out=bf(64, 80)), "out"),
     (lambda: qm.moe_dequantize_mx(u8(*Q), u8(*S), out=fake(64, 160, dtype=torch.float16)), "out"),
