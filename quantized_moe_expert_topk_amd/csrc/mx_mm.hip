@@ -13,8 +13,9 @@
 // Choices, with what they measured at 8192 x 4096 x 4096 unless another size is given:
 // - 32 x 32 x 64 instructions (mx_dev.h), a wave tile of 64 x 64: most products a byte read from LDS that leaves room for
 //   three stages; 256 x 256 tiles with two stages took as long (72, and 176 against 165 for 8 experts of 2048 rows).
-// - Four waves that only load beside eight that multiply (APART), for 256 x 128 tiles: 76 to 72, 8 experts of 2048 rows 184 to
-//   165.  Smaller tiles are bound by memory's latency, and load in the waves that multiply (1000 rows: 14 for 18).
+// - Four waves that only load, beside four or eight that multiply: 256 x 128 tiles 76 to 72, 8 experts of 2048 rows 184 to
+//   165; 128 x 128 tiles, four that multiply for eight that do both, 1000 x 4096 x 4096 13.8 to 12.2; 128 x 32, 64 rows 9.7
+//   to 8.8.
 // - Products pinned to their step (pin()): 92 to 81; loads beside all of a stage's steps: 81 to 77.
 // - Packed weights lie in LDS as in memory: 1 KB contiguous a load (prefill above 164 to 150), scales of a wave's two
 //   fragments in one operand (140 to 133).
@@ -60,30 +61,30 @@ struct MxTile {
   int e, p0, q0, rows;  // rows: output rows q0, q0 + 1, ... that exist
 };
 
-template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool APART, bool TILE16, bool OUT_BF16>
-__global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) void k_mx_product(MxArgs a) {
-  // APART: the first four waves load, and the others multiply; else every wave does both.
-  constexpr int W = APART ? 4 : WP * WQ, THREADS = 64 * W, TP = BP / WP / 32, TQ = BQ / WQ / 32;  // W: waves that load
+constexpr int kLoaders = 4;  // waves that only load
+
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool TILE16, bool OUT_BF16>
+__global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4) void k_mx_product(MxArgs a) {
+  constexpr int THREADS = 64 * kLoaders, TP = BP / WP / 32, TQ = BQ / WQ / 32;  // THREADS: that load
   using ATile = std::conditional_t<TILE16, PackedTile<BP, THREADS, TP>, RowTile<BP, THREADS>>;
   using BTile = RowTile<BQ, THREADS>;
   // Scales in LDS, a dword for each row: of the weights' first group of 128 columns, of their second, then of x.  A dword is
-  // four blocks of a row; of a packed bank's weights, one block of four rows, 16 rows x 4 blocks after one another.  Four
-  // waves load a group each, 16 bytes a lane: a load to LDS takes some 20 cycles of the CU whatever it brings (4 bytes a
+  // four blocks of a row; of a packed bank's weights, one block of four rows, 16 rows x 4 blocks after one another.  Each
+  // loading wave loads a group, 16 bytes a lane: a load to LDS takes some 20 cycles of the CU whatever it brings (4 bytes a
   // lane, 16 loads a stage instead of 4: 8 us more at 8192 x 4096 x 4096).
   constexpr int CODES = ATile::kBytes + BTile::kBytes, STAGE = CODES + (BP + BQ) * 8;
   constexpr int LOADS = ATile::NL + BTile::NL + 1;  // per thread and stage
-  static_assert(W >= 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
+  static_assert(kLoaders == 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
   static_assert(NS > 2 && TP <= 2, "a stage of time between a load and its use; scales of two fragments together");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   __shared__ int32_t first[kMaxExperts + 1];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mul = APART ? wave - 4 : wave, wp = mul % WP, wq = mul / WP, h = lane >> 5, r32 = lane & 31;
   const int units = a.K / 32;
   const uint32_t pitch = (uint32_t)units * 16;
 
   int q_total = (a.g.M + BQ - 1) / BQ;
-  if (a.g.offsets) q_total = make_tile_table<THREADS + (APART ? 64 * WP * WQ : 0)>(a.g, BQ, first);
+  if (a.g.offsets) q_total = make_tile_table<64 * (kLoaders + WP * WQ)>(a.g, BQ, first);
 
   // The tiles' order and the XCDs' shares of it are those of k_product.  (A quotient is computed in vector registers; what
   // comes of it has to be scalar again, for the loads' resources.)
@@ -111,113 +112,110 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
     }
   };
 
-  // ---- the loads
-  ATile at;
-  BTile bt;
-  if constexpr (TILE16)
-    at.init(pitch);
-  else
-    at.init(pitch, false);
-  bt.init(pitch, false);
-  i32x4g ra{}, rb{}, rs{};  // what is left of the tile's codes of w and x, and of the scales that this wave loads
-  int left = 0;             // 16-byte units of the contraction of the tile being loaded
-  int lt = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-  const bool of_w = wave < 2;
-  const int half = wave & 1;  // the group of 128 columns whose scales this wave loads (waves 4 and up: none)
-  const auto advance = [](i32x4g &r, uint64_t by) __attribute__((always_inline)) {
-    const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + by;
-    r[0] = (int)(uint32_t)at;
-    r[1] = (int)(uint32_t)(at >> 32);
-  };
-  const bool packed = TILE16 && of_w;
-  const uint64_t step_s = packed ? 128 : (uint64_t)(of_w ? a.w_rows : (long long)a.g.M) * 8;
-  auto start = [&](const MxTile &o) __attribute__((always_inline)) {
-    left = units;
-    const size_t w_row = (size_t)o.e * a.N + o.p0;
-    const int cols = min(BP, a.N - o.p0);
-    ra = range_rsrc(a.w + w_row * pitch, cols * pitch);
-    rb = range_rsrc(a.x + (size_t)o.q0 * pitch, o.rows * pitch);
-    if (packed)  // the scales of `cols` rows from the half's first block on
-      rs = range_rsrc(a.ws + w_row * units + half * 64, max(cols * units - half * 64, 0));
-    else if (of_w)
-      rs = range_rsrc(a.ws + (half * (size_t)a.w_rows + w_row) * 4, half * 4 < left ? cols * 4 : 0);
-    else
-      rs = range_rsrc(a.xs + (half * (size_t)a.g.M + o.q0) * 4, half * 4 < left ? o.rows * 4 : 0);
-  };
-  auto find_next = [&]() __attribute__((always_inline)) {
-    lt += gridDim.x;
-    MxTile o;
-    if (locate(lt, o)) {
-      start(o);
-    } else {  // the loads past the last tile fetch nothing
-      left = 0;
-      ra[2] = rb[2] = rs[2] = 0;
-    }
-  };
-  const uint32_t lds0 = lds_addr(lds), lds_wave = lds0 + wave * 1024;
-  const uint32_t s_off = packed ? (lane >> 2) * 16 * units + (lane & 3) * 16 : lane * 16;
-  const int s_block = packed ? half * 4 + (lane & 3) : 0;  // packed: past a row's last block lie the next 16 rows' scales
-  const int s_lanes = wave < 2 ? BP / 4 : wave < 4 ? BQ / 4 : 0;
-  const uint64_t s_mask = s_lanes == 64 ? ~0ull : (1ull << s_lanes) - 1;
-  const uint32_t s_dst = lds0 + CODES + (of_w ? half * BP : 2 * BP + half * BQ) * 4;
-  auto load = [&](int slot, int i) __attribute__((always_inline)) {
-    const uint32_t d = lds_wave + slot * STAGE;
-    if (i == 0)
-      load_to_lds16_masked(rs, s_block < left ? s_off : kNowhere, s_dst + slot * STAGE, s_mask);
-    else if (i <= ATile::NL)
-      at.template load<NT>(ra, d, i - 1, left);
-    else
-      bt.load(rb, d + ATile::kBytes, i - 1 - ATile::NL, left);
-  };
-  auto close = [&]() __attribute__((always_inline)) {
-    constexpr int STEP_A = TILE16 ? KB * 16 : KB;
-    left -= KB / 16;
-    advance(ra, STEP_A);
-    advance(rb, KB);
-    advance(rs, step_s);
-    ra[2] -= STEP_A;
-    rb[2] -= KB;
-    rs[2] = packed ? max(rs[2] - 128, 0) : half * 4 < left ? rs[2] : 0;
-    if (left <= 0) find_next();
-  };
-
-  // ---- the products
   MxTile o;
-  int ct = lt;
+  int ct = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
   if (!locate(ct, o)) return;
   const int n_stages = (units + KB / 16 - 1) / (KB / 16);
-  if constexpr (APART) {
-    if (wave < 4) {
-      // The waves meet once a stage (and once before the first): the next stage has been loaded, this one's slot read.
-      lt = ct;
-      start(o);
-#pragma unroll
-      for (int s = 0; s < NS; s++) {
-#pragma unroll
-        for (int i = 0; i < LOADS; i++) load(s, i);
-        close();
+  // The waves meet once before the first stage and once in each: the next stage has been loaded, this one's slot read.
+
+  if (wave < kLoaders) {
+    ATile at;
+    BTile bt;
+    if constexpr (TILE16)
+      at.init(pitch);
+    else
+      at.init(pitch, false);
+    bt.init(pitch, false);
+    i32x4g ra{}, rb{}, rs{};  // what is left of the tile's codes of w and x, and of the scales that this wave loads
+    int left = 0;             // 16-byte units of the contraction of the tile being loaded
+    int lt = ct;
+    const bool of_w = wave < 2;
+    const int half = wave & 1;  // the group of 128 columns whose scales this wave loads
+    const auto advance = [](i32x4g &r, uint64_t by) __attribute__((always_inline)) {
+      const uint64_t at = ((uint64_t)(uint32_t)r[1] << 32 | (uint32_t)r[0]) + by;
+      r[0] = (int)(uint32_t)at;
+      r[1] = (int)(uint32_t)(at >> 32);
+    };
+    const bool packed = TILE16 && of_w;
+    const uint64_t step_s = packed ? 128 : (uint64_t)(of_w ? a.w_rows : (long long)a.g.M) * 8;
+    auto start = [&](const MxTile &o) __attribute__((always_inline)) {
+      left = units;
+      const size_t w_row = (size_t)o.e * a.N + o.p0;
+      const int cols = min(BP, a.N - o.p0);
+      ra = range_rsrc(a.w + w_row * pitch, cols * pitch);
+      rb = range_rsrc(a.x + (size_t)o.q0 * pitch, o.rows * pitch);
+      if (packed)  // the scales of `cols` rows from the half's first block on
+        rs = range_rsrc(a.ws + w_row * units + half * 64, max(cols * units - half * 64, 0));
+      else if (of_w)
+        rs = range_rsrc(a.ws + (half * (size_t)a.w_rows + w_row) * 4, half * 4 < left ? cols * 4 : 0);
+      else
+        rs = range_rsrc(a.xs + (half * (size_t)a.g.M + o.q0) * 4, half * 4 < left ? o.rows * 4 : 0);
+    };
+    auto find_next = [&]() __attribute__((always_inline)) {
+      lt += gridDim.x;
+      MxTile o;
+      if (locate(lt, o)) {
+        start(o);
+      } else {  // the loads past the last tile fetch nothing
+        left = 0;
+        ra[2] = rb[2] = rs[2] = 0;
       }
-      wait_vm<(NS - 1) * LOADS>();
-      barrier_only();
-      int slot = 0;
-      for (;;) {
-        for (int s = 0; s < n_stages; s++) {
-          wait_vm<(NS - 2) * LOADS>();
-          barrier_only();
+    };
+    const uint32_t lds0 = lds_addr(lds), lds_wave = lds0 + wave * 1024;
+    const uint32_t s_off = packed ? (lane >> 2) * 16 * units + (lane & 3) * 16 : lane * 16;
+    const int s_block = packed ? half * 4 + (lane & 3) : 0;  // packed: past a row's last block lie the next 16 rows' scales
+    const int s_lanes = of_w ? BP / 4 : BQ / 4;
+    const uint64_t s_mask = s_lanes == 64 ? ~0ull : (1ull << s_lanes) - 1;
+    const uint32_t s_dst = lds0 + CODES + (of_w ? half * BP : 2 * BP + half * BQ) * 4;
+    auto load = [&](int slot, int i) __attribute__((always_inline)) {
+      const uint32_t d = lds_wave + slot * STAGE;
+      if (i == 0)
+        load_to_lds16_masked(rs, s_block < left ? s_off : kNowhere, s_dst + slot * STAGE, s_mask);
+      else if (i <= ATile::NL)
+        at.template load<NT>(ra, d, i - 1, left);
+      else
+        bt.load(rb, d + ATile::kBytes, i - 1 - ATile::NL, left);
+    };
+    auto close = [&]() __attribute__((always_inline)) {
+      constexpr int STEP_A = TILE16 ? KB * 16 : KB;
+      left -= KB / 16;
+      advance(ra, STEP_A);
+      advance(rb, KB);
+      advance(rs, step_s);
+      ra[2] -= STEP_A;
+      rb[2] -= KB;
+      rs[2] = packed ? max(rs[2] - 128, 0) : half * 4 < left ? rs[2] : 0;
+      if (left <= 0) find_next();
+    };
+
+    start(o);
 #pragma unroll
-          for (int i = 0; i < LOADS; i++) load(slot, i);
-          close();
-          slot = slot == NS - 1 ? 0 : slot + 1;
-        }
-        ct += gridDim.x;
-        if (!locate(ct, o)) break;
-      }
-      wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
-      return;
+    for (int s = 0; s < NS; s++) {
+#pragma unroll
+      for (int i = 0; i < LOADS; i++) load(s, i);
+      close();
     }
+    wait_vm<(NS - 1) * LOADS>();
+    barrier_only();
+    int slot = 0;
+    for (;;) {
+      for (int s = 0; s < n_stages; s++) {
+        wait_vm<(NS - 2) * LOADS>();
+        barrier_only();
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) load(slot, i);
+        close();
+        slot = slot == NS - 1 ? 0 : slot + 1;
+      }
+      ct += gridDim.x;
+      if (!locate(ct, o)) break;
+    }
+    wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
+    return;
   }
-  lt = ct;
-  if constexpr (!APART) start(o);
+
+  // ---- the waves that multiply
+  const int mul = wave - kLoaders, wp = mul % WP, wq = mul / WP, h = lane >> 5, r32 = lane & 31;
   f32x16_t acc[TP][TQ];
   // Step ks multiplies the units ks (lanes 0..31) and 4 + ks (lanes 32..63) of a stage: the scales of a lane's four steps are
   // then the bytes of one dword, which the instruction picks from (packed banks: those of the fragments).
@@ -238,18 +236,7 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
   const uint32_t sb_at = CODES + BP * 8 + h * BQ * 4 + wq * TQ * 128 + r32 * 4;
   uint4 af[2][TP], bf[2][TQ];
   uint32_t sa[2][TILE16 ? 1 : TP], sb[TQ], sb_next[TQ];  // sa: of a step (packed banks), or of this stage and the next one
-  // Before a stage's last step the waves meet: its slot has been read, and the next one is loaded.  The slot's loads then go
-  // out beside the four steps up to the next meeting, the first FIRST of them beside the first.
-  constexpr int FIRST = LOADS / NKS;
-  int slot = 0, fill = NS - 1, stored = 0;
-  constexpr int STORES = TP * TQ * (OUT_BF16 ? 2 : 4);
-  auto wait_loads = [&]() __attribute__((always_inline)) {
-    if (stored)  // (stores, and loads in front of the newest NS - 2 stages', end in order)
-      wait_vm<STORES + (NS - 2) * LOADS>();
-    else
-      wait_vm<(NS - 2) * LOADS>();
-    stored = 0;
-  };
+  int slot = 0;
   auto read = [&](int sl, int ks, int to, int i) __attribute__((always_inline)) {
     const uint8_t *t = lds + sl * STAGE;
     if (i < TQ) {
@@ -296,9 +283,7 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
       constexpr bool last = ks == NKS - 1;
       constexpr int cur = ks & 1;
       if constexpr (last) {
-        if constexpr (!APART) wait_loads();
         barrier_only();
-        fill = slot;
         read_scales(next);
       }
       constexpr int TICKS = NM > NR ? NM : NR;
@@ -311,15 +296,9 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
         static_for<r1 - r0>([&](auto r) __attribute__((always_inline)) {
           read(last ? next : slot, last ? 0 : ks + 1, cur ^ 1, r0 + r);
         });
-        if constexpr (!APART) {
-          constexpr int at = (ks + 1) % NKS * TICKS + i;  // ticks from the meeting on
-          constexpr int j0 = at * LOADS / (NKS * TICKS), j1 = (at + 1) * LOADS / (NKS * TICKS);
-          static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { load(fill, j0 + j); });
-        }
         __builtin_amdgcn_sched_barrier(0);
       });
       pin();
-      if constexpr (!APART && ks == NKS - 2) close();
       if constexpr (last) use_scales();
     });
     slot = next;
@@ -327,10 +306,9 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
 
   // D register j of a lane: i = 8 (j / 4) + 4 h + j % 4 of fragment p, row lane % 32 of q.  i of fragment p is column 32 p + i
   // of the wave's, or TP i + p (packed).  Lanes trade pieces of 16 bytes, so that four of them hold 64 consecutive bytes of
-  // a row: a wave issues exactly STORES stores of 16 bytes a lane where rows are whole such pieces (N a multiple of 8, or
-  // of 4 in fp32), whatever part of the tile exists (the resource refuses the rest).  Other rows take the same pieces where
-  // they lie, unaligned, and the last one element by element (60 experts, 5000 x 1001 x 1440: single elements 36 us, so
-  // 22; 1000 columns 19).
+  // a row.  The resource refuses what is not of the tile.  Rows that are not whole such pieces (N a multiple of 8, or of 4
+  // in fp32) take the same pieces where they lie, unaligned, and the last one element by element (60 experts, 5000 x 1001 x
+  // 1440: single elements 36 us, so 22; 1000 columns 19).
   auto store = [&]() __attribute__((always_inline)) {
     constexpr uint32_t OS = OUT_BF16 ? 2 : 4;
     constexpr int PIECE = 16 / OS;
@@ -423,26 +401,14 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
         }
       }
     };
-    if (a.N % PIECE != 0) {
+    if (a.N % PIECE != 0)
       put(std::integral_constant<int, -1>{});
-    } else {
-      if (a.write_through)
-        put(std::integral_constant<int, kWriteThrough>{});
-      else
-        put(std::integral_constant<int, 0>{});
-      stored = 1;
-    }
+    else if (a.write_through)
+      put(std::integral_constant<int, kWriteThrough>{});
+    else
+      put(std::integral_constant<int, 0>{});
   };
 
-  if constexpr (!APART) {
-#pragma unroll
-    for (int s = 0; s < NS; s++) {
-#pragma unroll
-      for (int i = 0; i < (s < NS - 1 ? LOADS : FIRST); i++) load(s, i);
-      if (s < NS - 1) close();
-    }
-    wait_vm<(NS - 2) * LOADS + FIRST>();
-  }
   barrier_only();
 #pragma unroll
   for (int i = 0; i < NR; i++) read(0, 0, 0, i);
@@ -460,12 +426,11 @@ __global__ __launch_bounds__(64 * (WP * WQ + (APART ? 4 : 0)), APART ? 3 : 2) vo
     ct += gridDim.x;
     if (!locate(ct, o)) break;
   }
-  if constexpr (!APART) wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
 }
 
 namespace {
 
-template <int BP, int BQ, int WP, int WQ, int NS, bool NT, bool APART>
+template <int BP, int BQ, int WP, int WQ, int NS, bool NT>
 hipError_t run_mx(MxArgs a, bool out_bf16, hipStream_t s) {
   a.p_tiles = (a.N + BP - 1) / BP;
   const long long q = a.g.offsets ? a.g.M / BQ + std::min(a.g.E, a.g.M) : (a.g.M + BQ - 1) / BQ;  // the most there can be
@@ -475,11 +440,10 @@ hipError_t run_mx(MxArgs a, bool out_bf16, hipStream_t s) {
   const long long tiles = (q + a.q_run - 1) / a.q_run * a.q_run * a.p_tiles;
   if (tiles > 0x40000000LL) return hipErrorInvalidConfiguration;
   constexpr int LDS = NS * ((BP + BQ) * (KB + 8)) + kMaxExperts * 4 + 256;
-  constexpr int PER_CU = std::min(163840 / LDS, WP * WQ == 4 ? 2 : 1);
-  const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * PER_CU);
+  const int grid = (int)std::min<long long>((tiles + 7) / 8 * 8, 256LL * (163840 / LDS));  // what the CUs' LDS holds
   const auto run = [&](auto packed, auto bf16) {
-    k_mx_product<BP, BQ, WP, WQ, NS, NT, APART, decltype(packed)::value, decltype(bf16)::value>
-        <<<grid, 64 * (WP * WQ + (APART ? 4 : 0)), 0, s>>>(a);
+    k_mx_product<BP, BQ, WP, WQ, NS, NT, decltype(packed)::value, decltype(bf16)::value>
+        <<<grid, 64 * (kLoaders + WP * WQ), 0, s>>>(a);
   };
   if (a.tile16)
     out_bf16 ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
@@ -495,7 +459,7 @@ template <size_t... I>
 static hipError_t run_mx_tile(int t, const MxArgs &a, bool out_bf16, hipStream_t s, std::index_sequence<I...>) {
   hipError_t e = hipErrorInvalidValue;
   (void)((t == (int)I && (e = run_mx<kMxTiles[I].bp, kMxTiles[I].bq, kMxTiles[I].wp, kMxTiles[I].wq, kMxTiles[I].stages,
-                                     kMxTiles[I].nt, kMxTiles[I].apart>(a, out_bf16, s), true)) || ...);
+                                     kMxTiles[I].nt>(a, out_bf16, s), true)) || ...);
   return e;
 }
 

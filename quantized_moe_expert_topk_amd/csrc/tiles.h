@@ -9,11 +9,10 @@
 
 namespace qmoe {
 
-// k_product's parameters: outputs a workgroup, waves along p and q, stages in LDS, weights non-temporal.  k_mx_product's
-// too, with whether waves of their own load.
+// k_product's parameters: outputs a workgroup, waves along p and q, stages in LDS, weights non-temporal.
 struct Tile {
   int bp, bq, wp, wq, stages;
-  bool nt, apart = false;
+  bool nt;
 };
 
 // The tiles that each product is built for; the choices below are places in these.
@@ -124,27 +123,27 @@ inline int choose_block(const ProductArgs &a, int rows) {
   return tiles(128) <= 256 ? 2 : 3;
 }
 
-// The MXFP4 products: k_mx_product's tiles (mx_mm.hip), or k_mx_few (mx_few.hip).
-inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true},   {128, 64, 4, 2, 5, true},   {128, 128, 2, 4, 4, false},
-                                    {256, 128, 4, 2, 3, false, true}, {256, 128, 4, 2, 3, true, true}};
+// The MXFP4 products: k_mx_product's tiles (mx_mm.hip; wp x wq waves multiply), or k_mx_few (mx_few.hip).
+inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4, false}, {256, 128, 4, 2, 3, false},
+                                    {256, 128, 4, 2, 3, true}};
 
 // Measured (MI355X, us).  k_mx_few costs 4.5 us and moves 3.9 bytes of weights a ns, once per 16 rows; 128 x 32 tiles, one
-// for each CU at most, 5 us and 0.22 a stage: 16 x 4096 x 4096 7.3 / 8.3, 64 rows 12.2 / 8.5, one row of 8 of 256 experts,
-// 1024 x 2048, 8.1 / 10.9.  Then the smallest tiles that one round over the CUs holds, whose stages take the least time:
+// for each CU at most, 5 us and 0.22 a stage: 16 x 4096 x 4096 7.0 / 9.0, 64 rows 8.8 / 8.8, one row of 8 of 256 experts,
+// 1024 x 2048, 8.1 / 10.9.  Then the smaller tiles where one round over the CUs holds them, whose stages take less time:
 //                            128 x 32   128 x 64   128 x 128   256 x 128
-//   256 x 4096 x 4096           11.2       11.3       11.9
-//   512 x 4096 x 4096           17.9       12.4       12.5        16.4
-//   1000 x 4096 x 4096          31.4       21.0       14.1        16.4
-//   2000 x 4096 x 4096          57.5       39.3       23.4        21.3
+//   256 x 4096 x 4096           10.0       10.2       10.3        15.7
+//   512 x 4096 x 4096           18.0       11.6       10.6        16.4
+//   1000 x 4096 x 4096          31.8       19.3       12.2        16.8
+//   2000 x 4096 x 4096                                21.4        18.5
 // and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
-// to read; non-temporal where the mean is two row tiles at most (nt; 8192 x 4096 x 4096 72 without, 87 with), unless rows end
+// to read; non-temporal where the mean is two row tiles at most (nt; 8192 x 4096 x 4096 68 without, 85 with), unless rows end
 // inside lines, which such loads fetch again (60 experts, 5000 x 1001 x 1440: 22 without, 28 with):
-//             128 x 32   128 x 64   256 x 128   256 x 128 nt
-//   m = 8        49.6       50.1       56.3         51.4
-//   m = 24       59.4       57.3       60.1         54.9
-//   m = 48       86.9       64.0       68.5         63.7
-//   m = 100     133.5       99.9       83.7         81.2
-//   m = 256, +- 260        201.6      133.1        130.8
+//             128 x 32   128 x 64   128 x 128   256 x 128   256 x 128 nt
+//   m = 8        48.6       49.6       53.4       56.3         51.4
+//   m = 24       59.0       54.6       58.4       60           54.9
+//   m = 48       85.0       62.7       65.4       67.6         61.3
+//   m = 100                            80.3       77.2         74.8
+//   m = 256, +- 260                   151        129          128
 inline int choose_mx(const MxArgs &a, int rows) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
   const auto q_tiles = [&](int bq) { return a.g.offsets ? (long long)rows / bq + std::min(a.g.E, rows) : ((long long)rows + bq - 1) / bq; };  // about
@@ -152,9 +151,8 @@ inline int choose_mx(const MxArgs &a, int rows) {
   const double few_mb = (double)q_tiles(16) * a.N * a.K * (17. / 32) / 1e6;
   if (few_mb < 3 + 0.86 * ((a.K + 255) / 256)) return kFewRows;
   if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return 0;
-  if (tiles(128, 64) <= 256) return 1;
-  if (tiles(128, 128) <= 256) return 2;
-  return a.g.offsets && mean <= 256 && (a.tile16 || a.K % 256 == 0) ? 4 : 3;
+  if (tiles(128, 128) <= 256) return 1;
+  return a.g.offsets && mean <= 256 && (a.tile16 || a.K % 256 == 0) ? 3 : 2;
 }
 
 // Whether k_product's outputs are stored non-temporal and written through to memory.  Nothing here reads them again, and

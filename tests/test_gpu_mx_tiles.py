@@ -24,9 +24,9 @@ CASES = {
     "32 rows": ([(5 * i) % 23 for i in range(64)], 1040, 2080),
     "32 rows, one stage": ([(5 * i) % 23 for i in range(64)], 1040, 160),
     "32 rows, dense": (200, 1040, 2080),
-    "64 rows": ([70, 0, 61, 130, 1, 200], 2064, 2080),
-    "64 rows, dense": (500, 2064, 2080),
-    "64 rows, dense, one stage": (1000, 1040, 256),
+    "100 rows": ([70, 0, 61, 130, 1, 200], 2064, 2080),
+    "100 rows, dense": (500, 2064, 2080),
+    "100 rows, dense, one stage": (1000, 1040, 256),
     "128 rows": ([300, 0, 700, 1, 290], 2064, 544),
     "128 rows, dense": (1300, 2064, 1056),
     "128 rows, dense, one stage": (1300, 2064, 224),
@@ -44,7 +44,7 @@ CASES = {
 # row-major weights of any N: rows that are not whole pieces of 16 bytes
 ODD = {
     "odd, 32 rows": ([(5 * i) % 23 for i in range(64)], 1001, 544),
-    "odd, 64 rows": (1000, 1037, 544),
+    "odd, dense": (1000, 1037, 544),
     "odd, 128 rows": ([300, 0, 700, 1, 290], 2055, 544),
     "odd, large": ([1900, 0, 1100, 2300, 1700], 2061, 288),
     "odd, many experts": ([(29 * i) % 331 for i in range(64)], 1026, 512),
