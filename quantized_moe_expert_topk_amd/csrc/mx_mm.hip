@@ -17,6 +17,8 @@
 //   165; 128 x 128 tiles, four that multiply for eight that do both, 1000 x 4096 x 4096 13.8 to 12.2; 128 x 32, 64 rows 9.7
 //   to 8.8.
 // - Products pinned to their step (pin()): 92 to 81; loads beside all of a stage's steps: 81 to 77.
+// - Fragments without rows are not multiplied: 256 experts of 24 rows 60 to 54, of 48 67 to 61, 32 of 200 rows 117 to 108,
+//   prefill above 134 to 131.
 // - Packed weights lie in LDS as in memory: 1 KB contiguous a load (prefill above 164 to 150), scales of a wave's two
 //   fragments in one operand (140 to 133).
 #include <algorithm>
@@ -75,7 +77,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
   constexpr int CODES = ATile::kBytes + BTile::kBytes, STAGE = CODES + (BP + BQ) * 8;
   constexpr int LOADS = ATile::NL + BTile::NL + 1;  // per thread and stage
   static_assert(kLoaders == 4 && BP <= 256 && BQ <= 256, "a wave for each group of scales");
-  static_assert(NS > 2 && TP <= 2, "a stage of time between a load and its use; scales of two fragments together");
+  static_assert(NS > 2 && TP <= 2 && TQ <= 2, "a stage of time between a load and its use; scales of two fragments together");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   __shared__ int32_t first[kMaxExperts + 1];
 
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
   f32x16_t acc[TP][TQ];
   // Step ks multiplies the units ks (lanes 0..31) and 4 + ks (lanes 32..63) of a stage: the scales of a lane's four steps are
   // then the bytes of one dword, which the instruction picks from (packed banks: those of the fragments).
-  constexpr int NKS = 4, NM = TP * TQ, NR = TP + TQ;
+  constexpr int NKS = 4;
   uint32_t a_at[TILE16 ? TP : NKS], b_at[NKS];  // a_at by fragment (packed), or by step
 #pragma unroll
   for (int ks = 0; ks < NKS; ks++) {  // (of fragment 0: the swizzle repeats every 16 rows)
@@ -237,12 +239,12 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
   uint4 af[2][TP], bf[2][TQ];
   uint32_t sa[2][TILE16 ? 1 : TP], sb[TQ], sb_next[TQ];  // sa: of a step (packed banks), or of this stage and the next one
   int slot = 0;
-  auto read = [&](int sl, int ks, int to, int i) __attribute__((always_inline)) {
+  auto read = [&](int sl, int ks, int to, int i) __attribute__((always_inline)) {  // i: TP of the weights', then of x
     const uint8_t *t = lds + sl * STAGE;
-    if (i < TQ) {
-      bf[to][i] = *reinterpret_cast<const uint4 *>(t + b_at[ks] + i * 32 * KB);
+    if (i >= TP) {
+      bf[to][i - TP] = *reinterpret_cast<const uint4 *>(t + b_at[ks] + (i - TP) * 32 * KB);
     } else {
-      const int p = i - TQ;
+      const int p = i;
       if constexpr (TILE16) {
         af[to][p] = *reinterpret_cast<const uint4 *>(t + a_at[p] + ks * 256);
         const uint8_t *s = t + sa_at + ks * 16;
@@ -277,7 +279,8 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
 #pragma unroll
       for (int q = 0; q < TQ; q++) asm volatile("" : "+v"(acc[p][q]));
   };
-  auto stage = [&]() __attribute__((always_inline)) {
+  auto stage = [&](auto live) __attribute__((always_inline)) {  // live: of the wave's TQ fragments of x
+    constexpr int LQ = live, NM = TP * LQ, NR = TP + LQ;
     const int next = slot == NS - 1 ? 0 : slot + 1;
     static_for<NKS>([&](auto ks) __attribute__((always_inline)) {
       constexpr bool last = ks == NKS - 1;
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
       constexpr int TICKS = NM > NR ? NM : NR;
       static_for<TICKS>([&](auto i) __attribute__((always_inline)) {
         if constexpr (i < NM) {
-          constexpr int p = i / TQ, q = i % TQ;
+          constexpr int p = i / LQ, q = i % LQ;
           acc[p][q] = mfma32_mx<TILE16 ? p : ks, ks>(af[cur][p], bf[cur][q], sa[TILE16 ? cur : 0][TILE16 ? 0 : p], sb[q], acc[p][q]);
         }
         constexpr int r0 = i * NR / TICKS, r1 = (i + 1) * NR / TICKS;
@@ -348,6 +351,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
       };
 #pragma unroll
       for (int q = 0; q < TQ; q++) {
+        if ((wq * TQ + q) * 32 >= o.rows) continue;
         const int row = (wq * TQ + q) * 32 + r16;
         // piece n of a lane, in the columns' order: PIECE elements from e(PIECE n) on
         const auto element = [&](int n) __attribute__((always_inline)) {
@@ -409,11 +413,14 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
       put(std::integral_constant<int, 0>{});
   };
 
-  barrier_only();
+  auto begin = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < NR; i++) read(0, 0, 0, i);
-  read_scales(0);
-  use_scales();
+    for (int i = 0; i < TP + TQ; i++) read(slot, 0, 0, i);
+    read_scales(slot);
+    use_scales();
+  };
+  barrier_only();
+  begin();
   for (;;) {
 #pragma unroll
     for (int p = 0; p < TP; p++)
@@ -421,10 +428,21 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
       for (int q = 0; q < TQ; q++)
 #pragma unroll
         for (int j = 0; j < 16; j++) acc[p][q][j] = 0.f;
-    for (int s = 0; s < n_stages; s++) stage();
+    const int live = (o.rows + 31 - wq * TQ * 32) / 32;  // fragments with rows
+    if (TQ == 1 || live >= TQ) {
+      for (int s = 0; s < n_stages; s++) stage(std::integral_constant<int, TQ>{});
+    } else if (live > 0) {
+      for (int s = 0; s < n_stages; s++) stage(std::integral_constant<int, 1>{});
+    } else {
+      for (int s = 0; s < n_stages; s++) {
+        barrier_only();
+        slot = slot == NS - 1 ? 0 : slot + 1;
+      }
+    }
     store();
     ct += gridDim.x;
     if (!locate(ct, o)) break;
+    if (TQ > 1 && live < TQ) begin();
   }
 }
 
