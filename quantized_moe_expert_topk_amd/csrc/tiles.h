@@ -130,20 +130,21 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 // Measured (MI355X, us).  k_mx_few costs 4.5 us and moves 3.9 bytes of weights a ns, once per 16 rows; 128 x 32 tiles, one
 // for each CU at most, 5 us and 0.22 a stage: 16 x 4096 x 4096 7.0 / 9.0, 64 rows 8.8 / 8.8, one row of 8 of 256 experts,
 // 1024 x 2048, 8.1 / 10.9.  Then the smaller tiles where one round over the CUs holds them, whose stages take less time:
-//                            128 x 32   128 x 64   128 x 128   256 x 128
-//   256 x 4096 x 4096           10.0       10.2       10.3        15.7
-//   512 x 4096 x 4096           18.0       11.6       10.6        16.4
-//   1000 x 4096 x 4096          31.8       19.3       12.2        16.8
-//   2000 x 4096 x 4096                                21.4        18.5
+//                            128 x 32   128 x 128   256 x 128
+//   256 x 4096 x 4096           10.2       10.6        14.3
+//   512 x 4096 x 4096           18.0       11.2        14.8
+//   1000 x 4096 x 4096          31.9       13.1        16.5
+//   2000 x 4096 x 4096          58         21.9        19.4
 // and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
-// to read; non-temporal where the mean is two row tiles at most (nt; 8192 x 4096 x 4096 68 without, 85 with), unless rows end
-// inside lines, which such loads fetch again (60 experts, 5000 x 1001 x 1440: 22 without, 28 with):
-//             128 x 32   128 x 64   128 x 128   256 x 128   256 x 128 nt
-//   m = 8        48.6       49.6       53.4       56.3         51.4
-//   m = 24       59.0       54.6       58.4       60           54.9
-//   m = 48       85.0       62.7       65.4       67.6         61.3
-//   m = 100                            80.3       77.2         74.8
-//   m = 256, +- 260                   151        129          128
+// to read, non-temporal where experts have two row tiles at most (nt), unless rows end inside lines, which such loads fetch again
+// (60 experts, 5000 x 1001 x 1440: 22 without, 27 with):
+//               128 x 32   128 x 128   256 x 128   256 x 128 nt
+//   m = 8          49         54          55           51
+//   m = 24         59         58          59           54
+//   m = 48         86         65          66           60
+//   m = 100       136         80          77           75
+//   m = 256       291        152         125          129
+//   m = 256, uneven (sizes' logarithms +- 1)  300   153   127   126
 inline int choose_mx(const MxArgs &a, int rows) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
   const auto q_tiles = [&](int bq) { return a.g.offsets ? (long long)rows / bq + std::min(a.g.E, rows) : ((long long)rows + bq - 1) / bq; };  // about

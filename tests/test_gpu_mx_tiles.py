@@ -37,8 +37,8 @@ CASES = {
     "large, dense, one stage": (9000, 4112, 256),
     "large, whole lines": ([1900, 0, 1100, 2300, 1700], 2048, 512),
     "many stages": ([901, 600, 1, 700], 2064, 8224),
-    "many experts": ([(29 * i) % 331 for i in range(64)], 1040, 2080),
-    "many experts, one stage": ([(29 * i) % 331 for i in range(64)], 1040, 64),
+    "many experts": ([(29 * i) % 231 for i in range(64)], 1040, 2080),
+    "many experts, one stage": ([(29 * i) % 231 for i in range(64)], 1040, 64),
     "many experts, whole stages": ([(29 * i) % 131 for i in range(64)], 1040, 1024),
 }
 # row-major weights of any N: rows that are not whole pieces of 16 bytes
@@ -47,7 +47,7 @@ ODD = {
     "odd, dense": (1000, 1037, 544),
     "odd, 128 rows": ([300, 0, 700, 1, 290], 2055, 544),
     "odd, large": ([1900, 0, 1100, 2300, 1700], 2061, 288),
-    "odd, many experts": ([(29 * i) % 331 for i in range(64)], 1026, 512),
+    "odd, many experts": ([(29 * i) % 231 for i in range(64)], 1026, 512),
     "narrow": (5000, 3, 288),
     "one column": (70, 1, 64),
 }
