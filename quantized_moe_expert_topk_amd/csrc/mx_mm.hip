@@ -88,12 +88,15 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
   int q_total = (a.g.M + BQ - 1) / BQ;
   if (a.g.offsets) q_total = make_tile_table<64 * (kLoaders + WP * WQ)>(a.g, BQ, first);
 
-  // The tiles' order and the XCDs' shares of it are those of k_product.  (A quotient is computed in vector registers; what
-  // comes of it has to be scalar again, for the loads' resources.)
+  // The tiles' order and the XCDs' shares of it are those of k_product.  Of a grid made for more rows than there are, the
+  // first workgroups of each XCD take the one round of tiles (16 experts of one row, M = 256, 1024 x 2048: 11.5 us if the
+  // first XCDs take it, so 7.8; the last of several rounds goes to the first XCDs, 256 experts of 48 rows 60, to all 64).
+  // (A quotient is computed in vector registers; what comes of it has to be scalar again, for the loads' resources.)
   const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int band = a.q_run * a.p_tiles;
+  const int grid = uniform(min((int)gridDim.x, ((q_total + a.q_run - 1) / a.q_run * band + 7) / 8 * 8));
   auto locate = [&](int &t, MxTile &o) __attribute__((always_inline)) {
-    const int band = a.q_run * a.p_tiles;
-    for (;; t += gridDim.x) {
+    for (;; t += grid) {
       const int bq = uniform(t / band);
       if (bq * a.q_run >= q_total) return false;
       const int r = t - bq * band, pt = uniform(r / a.q_run), qt = bq * a.q_run + r - pt * a.q_run;
@@ -115,8 +118,8 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
   };
 
   MxTile o;
-  int ct = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
-  if (!locate(ct, o)) return;
+  int ct = blockIdx.x % 8 * (grid / 8) + blockIdx.x / 8;
+  if ((int)blockIdx.x >= grid || !locate(ct, o)) return;
   const int n_stages = (units + KB / 16 - 1) / (KB / 16);
   // The waves meet once before the first stage and once in each: the next stage has been loaded, this one's slot read.
 
@@ -154,7 +157,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
         rs = range_rsrc(a.xs + (half * (size_t)a.g.M + o.q0) * 4, half * 4 < left ? o.rows * 4 : 0);
     };
     auto find_next = [&]() __attribute__((always_inline)) {
-      lt += gridDim.x;
+      lt += grid;
       MxTile o;
       if (locate(lt, o)) {
         start(o);
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
         close();
         slot = slot == NS - 1 ? 0 : slot + 1;
       }
-      ct += gridDim.x;
+      ct += grid;
       if (!locate(ct, o)) break;
     }
     wait_vm<0>();  // the loads past the last stage still write (zeros) to LDS
@@ -440,7 +443,7 @@ __global__ __launch_bounds__(64 * (kLoaders + WP * WQ), (kLoaders + WP * WQ) / 4
       }
     }
     store();
-    ct += gridDim.x;
+    ct += grid;
     if (!locate(ct, o)) break;
     if (TQ > 1 && live < TQ) begin();
   }

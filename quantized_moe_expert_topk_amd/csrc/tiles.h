@@ -147,7 +147,11 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   m = 256, uneven (sizes' logarithms +- 1)  300   153   127   126
 inline int choose_mx(const MxArgs &a, int rows) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
-  const auto q_tiles = [&](int bq) { return a.g.offsets ? (long long)rows / bq + std::min(a.g.E, rows) : ((long long)rows + bq - 1) / bq; };  // about
+  // row tiles, about: an expert's last one is half full, and each has one
+  const long long experts = std::min(a.g.E, rows);
+  const auto q_tiles = [&](int bq) {
+    return a.g.offsets ? std::max(experts, rows / bq + experts / 2) : ((long long)rows + bq - 1) / bq;
+  };
   const auto tiles = [&](int bp, int bq) { return q_tiles(bq) * ((a.N + bp - 1LL) / bp); };
   const double few_mb = (double)q_tiles(16) * a.N * a.K * (17. / 32) / 1e6;
   if (few_mb < 3 + 0.86 * ((a.K + 255) / 256)) return kFewRows;
