@@ -127,14 +127,19 @@ inline int choose_block(const ProductArgs &a, int rows) {
 inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4, false}, {256, 128, 4, 2, 3, false},
                                     {256, 128, 4, 2, 3, true}};
 
-// Measured (MI355X, us).  k_mx_few costs 4.5 us and moves 3.9 bytes of weights a ns, once per 16 rows; 128 x 32 tiles, one
-// for each CU at most, 5 us and 0.22 a stage: 16 x 4096 x 4096 7.0 / 9.0, 64 rows 8.8 / 8.8, one row of 8 of 256 experts,
-// 1024 x 2048, 8.1 / 10.9.  Then the smaller tiles where one round over the CUs holds them, whose stages take less time:
+// Measured (MI355X, us).  Launches of a graph, k_mx_few / 128 x 32 tiles:
+//   dense   16 x 1024 x 2048 3.8 / 5.0   16 x 4096 x 4096 4.8 / 6.8   64 x 2048 x 4096 7.3 / 7.2   32 x 512 x 8192 6.8 / 11.7
+//   one token, 8 of 256 experts   512 x 4096 5.8 / 9.9   1024 x 2048 7.1 / 7.1   2048 x 512 8.2 / 5.1   4096 x 2048 13.1 / 11.1
+//   two tokens                   1024 x 2048 9.4 / 7.9   128 rows to 8 experts   512 x 7168 9.3 / 15.2
+// k_mx_few takes a time for what it reads, by 16 rows of weights and of x, and by expert for each of its tiles; the other for
+// each stage, if the CUs hold all tiles at once.  Then the smaller tiles where one round over the CUs holds them, whose
+// stages take less time:
 //                            128 x 32   128 x 128   256 x 128
 //   256 x 4096 x 4096           10.2       10.6        14.3
 //   512 x 4096 x 4096           18.0       11.2        14.8
 //   1000 x 4096 x 4096          31.9       13.1        16.5
 //   2000 x 4096 x 4096          58         21.9        19.4
+//   8 of 16 experts, 2048 x 7168  19.3     13.5        25.9   (more in flight, which many stages pay for; 4096: 13.4 / 13.5)
 // and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
 // to read, non-temporal where experts have two row tiles at most (nt), unless rows end inside lines, which such loads fetch again
 // (60 experts, 5000 x 1001 x 1440: 22 without, 27 with):
@@ -144,7 +149,7 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   m = 48         86         65          66           60
 //   m = 100       136         80          77           75
 //   m = 256       291        152         125          129
-//   m = 256, uneven (sizes' logarithms +- 1)  300   153   127   126
+//   m = 256,      300        153         127          126   (uneven, logarithms of the sizes +- 1)
 inline int choose_mx(const MxArgs &a, int rows) {
   const int mean = a.g.offsets ? rows / std::max(1, std::min(a.g.E, rows)) : a.g.M;
   // row tiles, about: an expert's last one is half full, and each has one
@@ -153,10 +158,11 @@ inline int choose_mx(const MxArgs &a, int rows) {
     return a.g.offsets ? std::max(experts, rows / bq + experts / 2) : ((long long)rows + bq - 1) / bq;
   };
   const auto tiles = [&](int bp, int bq) { return q_tiles(bq) * ((a.N + bp - 1LL) / bp); };
-  const double few_mb = (double)q_tiles(16) * a.N * a.K * (17. / 32) / 1e6;
-  if (few_mb < 3 + 0.86 * ((a.K + 255) / 256)) return kFewRows;
-  if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return 0;
-  if (tiles(128, 128) <= 256) return 1;
+  const double few = (double)q_tiles(16) * ((a.N + 15) / 16), mb = few * a.K * (17. / 2) / 1e6, stages = (a.K + 255) / 256;
+  if (a.g.offsets ? 0.0033 * few + 0.09 * mb < 0.2 + 0.34 * stages : 0.26 * mb < 0.8 + 0.22 * stages) return kFewRows;
+  const bool once = tiles(128, 128) <= 256;
+  if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return once && stages > 16 ? 1 : 0;
+  if (once) return 1;
   return a.g.offsets && mean <= 256 && (a.tile16 || a.K % 256 == 0) ? 3 : 2;
 }
 
