@@ -88,7 +88,8 @@ def _room(rows: int | None, T: int, k: int) -> int:
 def moe_gather_rows(x: torch.Tensor, slots: torch.Tensor, rows: int | None = None, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """out[slots[t, j]] = x[t] for every pair.  x [T, H] of any type, rows of whole 16 bytes -> [rows, H] (``rows``: that
-    of ``out``, else T * k).  Its gradient for x is :func:`moe_combine_rows` of the rows' gradients, without weights."""
+    of ``out``, else T * k).  The bytes are moved as they are: a lazily conjugated view (``resolve_conj()``) is refused.
+    Its gradient for x is :func:`moe_combine_rows` of the rows' gradients, without weights."""
     T, H = shape = _sizes(x, "x")
     dev = x.device
     px = _arg(x, x.dtype, shape, dev, "x")
@@ -98,6 +99,10 @@ def moe_gather_rows(x: torch.Tensor, slots: torch.Tensor, rows: int | None = Non
         out = _empty((M, H), x.dtype, dev, stream)
     else:
         M = _sizes(out, "out")[0]
+    if x.dtype.is_complex:
+        for name, t in (("x", x), ("out", out)):
+            if t.is_conj():
+                raise ValueError(f"{name}: a conjugated view, whose bytes are not its values; call resolve_conj() first")
     width = H * x.element_size()
     if width > _INT_MAX:
         raise ValueError(f"x: rows of {width} bytes are too large for 32-bit sizes")
