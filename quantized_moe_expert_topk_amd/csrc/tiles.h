@@ -131,9 +131,15 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   dense   16 x 1024 x 2048 3.8 / 5.0   16 x 4096 x 4096 4.8 / 6.8   64 x 2048 x 4096 7.3 / 7.2   32 x 512 x 8192 6.8 / 11.7
 //   one token, 8 of 256 experts   512 x 4096 5.8 / 9.9   1024 x 2048 7.1 / 7.1   2048 x 512 8.2 / 5.1   4096 x 2048 13.1 / 11.1
 //   two tokens                   1024 x 2048 9.4 / 7.9   128 rows to 8 experts   512 x 7168 9.3 / 15.2
-// k_mx_few takes a time for what it reads, by 16 rows of weights and of x, and by expert for each of its tiles; the other for
-// each stage, if the CUs hold all tiles at once.  Then the smaller tiles where one round over the CUs holds them, whose
-// stages take less time:
+// Dense with weights that are not in the caches, k_mx_few / the best of the tiles:
+//   1 row   4096 x 4096 4.5 / 8.8   8192 x 4096 6.1 / 8.8   8192 x 14336 14.1 / 19.8
+//   16      8192 x 4096 7.9 / 8.8   4096 x 14336 11.9 / 19.5      64   4096 x 256 5.8 / 3.8   4096 x 2048 8.8 / 6.4
+//   256     512 x 512 4.2 / 4.1     512 x 4096 7.3 / 9.0     500  1024 x 128 7.9 / 3.8     2000  1800 x 32 36 / 6.2
+// k_mx_few takes a time for each of its tiles, 16 rows of weights by 16 of x, and for what they read (a dense one for the rows
+// of x that there are, too); the other for each stage, if the CUs hold all tiles at once.  (The dense constants are the best
+// of a grid of 678 sizes, 1 to 8192 rows, 32 to 14336 columns, in both layouts: 13 of those and of 565 others lose more than
+// a tenth to the best kernel, two more than a quarter.)  Then the smaller tiles where one round over the CUs holds them,
+// whose stages take less time:
 //                            128 x 32   128 x 128   256 x 128
 //   256 x 4096 x 4096           10.2       10.6        14.3
 //   512 x 4096 x 4096           18.0       11.2        14.8
@@ -159,7 +165,9 @@ inline int choose_mx(const MxArgs &a, int rows) {
   };
   const auto tiles = [&](int bp, int bq) { return q_tiles(bq) * ((a.N + bp - 1LL) / bp); };
   const double few = (double)q_tiles(16) * ((a.N + 15) / 16), mb = few * a.K * (17. / 2) / 1e6, stages = (a.K + 255) / 256;
-  if (a.g.offsets ? 0.0033 * few + 0.09 * mb < 0.2 + 0.34 * stages : 0.26 * mb < 0.8 + 0.22 * stages) return kFewRows;
+  const double mb_x = mb * std::min(rows, 16) / 16;
+  if (a.g.offsets ? 0.0033 * few + 0.09 * mb < 0.2 + 0.34 * stages : 0.002 * few + 0.12 * (mb + mb_x) < 0.4 + 0.36 * stages)
+    return kFewRows;
   const bool once = tiles(128, 128) <= 256;
   if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return once && stages > 16 ? 1 : 0;
   if (once) return 1;
