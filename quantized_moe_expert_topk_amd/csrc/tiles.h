@@ -145,7 +145,16 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   512 x 4096 x 4096           18.0       11.2        14.8
 //   1000 x 4096 x 4096          31.9       13.1        16.5
 //   2000 x 4096 x 4096          58         21.9        19.4
-//   8 of 16 experts, 2048 x 7168  19.3     13.5        25.9   (more in flight, which many stages pay for; 4096: 13.4 / 13.5)
+// but from 17 stages on (K > 4096) 128 x 128, if one round holds those: its stages are four deep, not three, and take 0.31 us for
+// 0.43 (64 x 4096), which pays for the 0.9 us that one stage takes longer:
+//                         128 x 32 / 128 x 128      K = 4096       4352          7168         14336
+//   dense   1 x 8192                               9.7 / 8.8   10.3 / 8.9   14.8 / 11.7   26.7 / 19.8
+//   dense   64 x 4096                              9.6 / 9.5   10.2 / 9.9   14.7 / 13.2   26.7 / 22.0
+//   dense   128 x 1024                             8.3 / 10.0   9.5 / 10.3  13.8 / 14.4   25.6 / 24.9
+//   dense   256 x 4096                            10.5 / 10.8  11.3 / 11.2  16.6 / 14.9   30.0 / 24.9
+//   16 rows of 8 experts, 2048                    10.9 / 11.2  12.1 / 10.9  16.8 / 13.4   28.9 / 22.1
+//   geometric mean of 128 x 128 over 128 x 32 where the rule decides between them, at 4352, 7168 and 14336: dense (18 sizes
+//   each) 0.96, 0.90, 0.85, at most 1.12; grouped (140 in all, 1 to 600 rows) 0.98, 0.95, 0.83, at most 1.16
 // and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
 // to read, non-temporal where experts have two row tiles at most (nt), unless rows end inside lines, which such loads fetch again
 // (60 experts, 5000 x 1001 x 1440: 22 without, 27 with):

@@ -31,3 +31,8 @@ def test_many_tiles_of_a_short_contraction(tiles):  # noqa: F811
     for M, N, K in itertools.product([1, 16, 90, 600, 5000, 100000], [16, 112, 1024, 8192, 65536], [32, 96, 256, 512]):
         if -(-M // 16) * -(-N // 16) >= 600:
             assert choice(tiles, (M, N, K), 0) != FEW_ROWS, (M, N, K)
+
+@pytest.mark.parametrize("size,want", [((64, 4096, 4096), 0), ((64, 4096, 4352), 1), ((64, 4096, 14336), 1), ((256, 4096, 4096), 0),
+                                       ((256, 4096, 7168), 1)], ids=str)
+def test_long_contractions_take_the_larger_tile(tiles, size, want):  # noqa: F811
+    assert choice(tiles, size, 0) == want
