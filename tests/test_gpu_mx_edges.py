@@ -14,6 +14,7 @@ import torch
 import quantized_moe_expert_topk_amd as qm
 from tests.test_gpu_grouped import check, gen, ranges, rows_of
 from tests.test_gpu_mx import ROWS, TILE16, decode, group, operand, tile16
+from tests.test_gpu_rows import some_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +211,22 @@ BIG, SMALL = 2 ** 31 - 1, -2 ** 31
 def test_ranges_that_are_not_ranges(layout, hint, off, cnt):
     """Whatever the device arrays hold, nothing outside y is written, and the call ends."""
     ranged(layout, off, cnt, hint)
+
+
+# ------------------------------------------------------------------------------------------- another stream
+
+def test_rows_quantised_into_slots_on_a_stream_of_their_own():
+    """Every row has its pair, so all of both outputs is compared."""
+    T, k, K = 100, 3, 512
+    x = torch.randn(T, K, device=DEV, generator=gen(2)).to(torch.bfloat16)
+    slots = some_slots(T, k, T * k, 2, lost=0.0)
+    want = [t.clone() for t in qm.moe_quantize_mx(x, slots)]
+    torch.cuda.synchronize()
+    S = torch.cuda.Stream()
+    with torch.cuda.stream(S):
+        got = qm.moe_quantize_mx(x, slots, stream=S)
+    S.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q, s = qm.moe_quantize_mx(x)
+    at = slots.view(-1).long()
+    assert torch.equal(want[0][at], q.repeat_interleave(k, 0)) and torch.equal(want[1][:, at], s.repeat_interleave(k, 1))
