@@ -6,20 +6,16 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "grouped_dev.h"
+#include "rows_dev.h"
 #include "tiles.h"
 
 namespace qmoe {
 namespace {
 
-constexpr int kWaves = 4, kMaxGroups = 1 << 20;
-
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 }  // namespace
 
@@ -66,19 +62,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_quantize_mx(const uint16_t *x, 
   }
 }
 
-// NT: non-temporal stores, where rows are whole lines (whole_lines(); rows.hip measures both).  65536 x 2048 bf16: 81 us
-// without, 64 with.
 template <bool OUT_F32, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, int K,
                                                                uint8_t *y) {
   const int c = blockIdx.y * 512 + lane_id() * 8;
   if (c >= K) return;
-  const auto store = [](auto *p, auto v) __attribute__((always_inline)) {
-    if constexpr (NT)
-      __builtin_nontemporal_store(v, p);
-    else
-      *p = v;
-  };
   for (int64_t r = blockIdx.x * kWaves + wave_id(); r < M; r += gridDim.x * kWaves) {
     const uint32_t codes = *reinterpret_cast<const uint32_t *>(q + ((size_t)r * K + c) / 2);
     const uint32_t b = scale[((size_t)(c / 128) * M + r) * 4 + c / 32 % 4];
@@ -89,14 +77,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q,
     const size_t at = (size_t)r * K + c;
     if constexpr (OUT_F32) {
       f32x4_t *o = reinterpret_cast<f32x4_t *>(y + at * 4);
-      store(o, f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s});
-      store(o + 1, f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s});
+      store_vec<NT>(o, f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s});
+      store_vec<NT>(o + 1, f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s});
     } else {
       typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
       u32x4 o;
 #pragma unroll
       for (int i = 0; i < 4; i++) o[i] = __builtin_bit_cast(uint32_t, pack_bf16(f[i][0] * s, f[i][1] * s));
-      store(reinterpret_cast<u32x4 *>(y + at * 2), o);
+      store_vec<NT>(reinterpret_cast<u32x4 *>(y + at * 2), o);
     }
   }
 }

@@ -9,7 +9,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "grouped_dev.h"
+#include "rows_dev.h"
 #include "tiles.h"
 
 namespace qmoe {
@@ -17,25 +17,9 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;          // of a workgroup
-constexpr int kMaxGroups = 1 << 20;  // workgroups along x; more tokens take several turns each
-
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
-
 template <class T>
 __device__ __forceinline__ T read_lane(T v, int lane) {
   return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-
-// Stores are non-temporal where rows are whole lines (whole_lines()): nothing here reads them again.  8192 tokens of 2048
-// bf16 to 8 of 256 experts, us: gather 61 without, 53 with; combine 66, 63; gradients 120, 115.  Rows of 1040 bytes 14
-// without, 21 with: lines that two rows share are then written in parts.
-template <bool NT, class V>
-__device__ __forceinline__ void store_vec(V *p, V v) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(v, p);
-  else
-    *p = v;
 }
 
 // N consecutive elements of one row, 16 bytes in memory per 4 (fp32) or 8 (bf16).
