@@ -62,9 +62,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_quantize_mx(const uint16_t *x, 
   }
 }
 
+// NT: non-temporal stores, of bf16 only (values_non_temporal()).
 template <bool OUT_F32, bool NT>
 __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, int K,
                                                                uint8_t *y) {
+  static_assert(!(OUT_F32 && NT), "a wave's fp32 stores leave gaps");
   const int c = blockIdx.y * 512 + lane_id() * 8;
   if (c >= K) return;
   for (int64_t r = blockIdx.x * kWaves + wave_id(); r < M; r += gridDim.x * kWaves) {
@@ -77,8 +79,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_dequantize_mx(const uint8_t *q,
     const size_t at = (size_t)r * K + c;
     if constexpr (OUT_F32) {
       f32x4_t *o = reinterpret_cast<f32x4_t *>(y + at * 4);
-      store_vec<NT>(o, f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s});
-      store_vec<NT>(o + 1, f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s});
+      o[0] = f32x4_t{f[0][0] * s, f[0][1] * s, f[1][0] * s, f[1][1] * s};
+      o[1] = f32x4_t{f[2][0] * s, f[2][1] * s, f[3][0] * s, f[3][1] * s};
     } else {
       typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
       u32x4 o;
@@ -101,11 +103,12 @@ hipError_t launch_dequantize_mx(const uint8_t *q, const uint8_t *scale, int M, i
   const auto run = [&](auto f32, auto nt) {
     k_dequantize_mx<decltype(f32)::value, decltype(nt)::value><<<grid, 64 * kWaves, 0, s>>>(q, scale, M, K, static_cast<uint8_t *>(y));
   };
-  const bool nt = whole_lines(y, K * (out_f32 ? 4LL : 2LL));
-  if (out_f32)
-    nt ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
+  if (values_non_temporal(y, K, out_f32))
+    run(std::false_type{}, std::true_type{});
+  else if (out_f32)
+    run(std::true_type{}, std::false_type{});
   else
-    nt ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
+    run(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 

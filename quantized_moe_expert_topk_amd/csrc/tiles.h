@@ -192,6 +192,11 @@ inline int choose_mx(const MxArgs &a, int rows) {
 inline bool whole_lines(const void *out, long long pitch) {
   return pitch % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
 }
+// The values of quantised rows (mx.hip): a lane has 8 of them, 16 bytes of bf16, and a wave writes whole lines; in fp32 two
+// stores of a wave write 16 of every 32 bytes each, and lines that go to memory in parts cost more than the caches do (us, non-
+// temporal / not: bf16 8192 x 4096 12.9 / 20.1, 65536 x 2048 74 / 81; fp32 2048 x 4096 12.5 / 10.8, 8192 x 4096 58 / 36.5, 16384 x
+// 4096 126 / 67).
+inline bool values_non_temporal(const void *y, int K, bool out_f32) { return !out_f32 && whole_lines(y, K * 2LL); }
 inline bool stores_go_through(const void *out, double bytes, long long pitch) {
   return bytes > 16e6 && whole_lines(out, pitch);
 }
