@@ -131,15 +131,19 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   dense   16 x 1024 x 2048 3.8 / 5.0   16 x 4096 x 4096 4.8 / 6.8   64 x 2048 x 4096 7.3 / 7.2   32 x 512 x 8192 6.8 / 11.7
 //   one token, 8 of 256 experts   512 x 4096 5.8 / 9.9   1024 x 2048 7.1 / 7.1   2048 x 512 8.2 / 5.1   4096 x 2048 13.1 / 11.1
 //   two tokens                   1024 x 2048 9.4 / 7.9   128 rows to 8 experts   512 x 7168 9.3 / 15.2
-// Dense with weights that are not in the caches, k_mx_few / the best of the tiles:
+//   packed / row-major weights   5 experts, 100 rows, 2048 x 7168: 20 / 30, 128 x 128 13.6 / 13.9   8, 8 rows, 512 x 4096: 5.0 / 5.6,
+//                                9.8 / 10.6   8, 256 rows, 1024 x 14336: 33 / 44, 128 x 128 22.4 / 23.2
+// Dense, four sets of inputs in turn, k_mx_few / the best of the tiles:
 //   1 row   4096 x 4096 4.5 / 8.8   8192 x 4096 6.1 / 8.8   8192 x 14336 14.1 / 19.8
 //   16      8192 x 4096 7.9 / 8.8   4096 x 14336 11.9 / 19.5      64   4096 x 256 5.8 / 3.8   4096 x 2048 8.8 / 6.4
 //   256     512 x 512 4.2 / 4.1     512 x 4096 7.3 / 9.0     500  1024 x 128 7.9 / 3.8     2000  1800 x 32 36 / 6.2
 // k_mx_few takes a time for each of its tiles, 16 rows of weights by 16 of x, and for what they read (a dense one for the rows
-// of x that there are, too); the other for each stage, if the CUs hold all tiles at once.  (The dense constants are the best
-// of a grid of 678 sizes, 1 to 8192 rows, 32 to 14336 columns, in both layouts: 13 of those and of 565 others lose more than
-// a tenth to the best kernel, two more than a quarter.)  Then the smaller tiles where one round over the CUs holds them,
-// whose stages take less time:
+// of x that there are, too; row-major weights of experts longer than packed ones); the other for each stage, if the CUs hold
+// all tiles at once.  The constants are the best of grids.  Dense, 678 sizes of 1 to 8192 rows and 32 to 14336 columns in both
+// layouts: 13 of those and of 565 others lose more than a tenth to the best kernel, two more than a quarter.  Grouped, 3312 sizes
+// of 1 to 256 experts, 1 to 600 rows, 64 to 14336 columns in each layout: about 60 of each lose more than a tenth, the
+// most 1.32.
+// Then the smaller tiles where one round over the CUs holds them, whose stages take less time:
 //                            128 x 32   128 x 128   256 x 128
 //   256 x 4096 x 4096           10.2       10.6        14.3
 //   512 x 4096 x 4096           18.0       11.2        14.8
@@ -154,7 +158,7 @@ inline constexpr Tile kMxTiles[] = {{128, 32, 4, 1, 3, true}, {128, 128, 2, 2, 4
 //   dense   256 x 4096                            10.5 / 10.8  11.3 / 11.2  16.6 / 14.9   30.0 / 24.9
 //   16 rows of 8 experts, 2048                    10.9 / 11.2  12.1 / 10.9  16.8 / 13.4   28.9 / 22.1
 //   geometric mean of 128 x 128 over 128 x 32 where the rule decides between them, at 4352, 7168 and 14336: dense (18 sizes
-//   each) 0.96, 0.90, 0.85, at most 1.12; grouped (140 in all, 1 to 600 rows) 0.98, 0.95, 0.83, at most 1.16
+//   each) 0.96, 0.90, 0.85, at most 1.12; grouped (409 in all, 1 to 600 rows) 0.98, 0.92, 0.86, at most 1.12
 // and for more the fewest bytes per product.  Many experts of m rows, 1024 x 2048, packed: the weights are the most there is
 // to read, non-temporal where experts have two row tiles at most (nt), unless rows end inside lines, which such loads fetch again
 // (60 experts, 5000 x 1001 x 1440: 22 without, 27 with):
@@ -175,7 +179,9 @@ inline int choose_mx(const MxArgs &a, int rows) {
   const auto tiles = [&](int bp, int bq) { return q_tiles(bq) * ((a.N + bp - 1LL) / bp); };
   const double few = (double)q_tiles(16) * ((a.N + 15) / 16), mb = few * a.K * (17. / 2) / 1e6, stages = (a.K + 255) / 256;
   const double mb_x = mb * std::min(rows, 16) / 16;
-  if (a.g.offsets ? 0.0033 * few + 0.09 * mb < 0.2 + 0.34 * stages : 0.002 * few + 0.12 * (mb + mb_x) < 0.4 + 0.36 * stages)
+  if (!a.g.offsets ? 0.002 * few + 0.12 * (mb + mb_x) < 0.4 + 0.36 * stages
+      : a.tile16   ? 0.0033 * few + 0.09 * mb < 0.6 + 0.28 * stages
+                   : 0.001 * few + 0.14 * mb < 0.2 + 0.2 * stages)
     return kFewRows;
   const bool once = tiles(128, 128) <= 256;
   if ((a.g.offsets && mean <= 16) || tiles(128, 32) <= 256) return once && stages > 16 ? 1 : 0;
