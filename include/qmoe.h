@@ -483,7 +483,8 @@ int moe_combine_rows_grad(const void *dout, int dout_dtype, const void *rows, in
 
 /* moe_quantize_mx -- bf16 rows to quantised rows:
  *   X[t, b] = the least power of two, at least 2^-126, with max |x[t, k]| <= 6 X over the 32 k of block b (nothing
- *             saturates; a block of zeros has 2^-126)
+ *             saturates; a block of zeros has 2^-126).  The OCP MX conversion, 2^(floor(log2 max) - 2), is half of X where the
+ *             largest is above 1.5 times a power of two, and saturates there; its rows are valid operands too.
  *   q = e2m1(x / X), rounded to nearest, ties to the even code; -0 and what rounds to it keep their sign.
  * A NaN or infinity in a block makes its scale 255 and its codes 0.
  *   slots  [T, k] as for moe_gather_rows: token t is quantised once and written to rows slots[t, :]; other rows of q and

@@ -1,5 +1,6 @@
 // grouped_dev.h -- device building blocks of the grouped products by expert and the fp8 block
-// products (grouped_mm.hip, block_mm.hip), gfx950.
+// products (grouped_mm.hip, block_mm.hip, few_rows.hip), gfx950.  The MXFP4 products (mx_mm.hip, mx_few.hip) use
+// its row ranges, operand tiles and loads, the rows' kernels (rows_dev.h) its row ranges.
 //
 // Every product is D[p, q] = sum_c A[p, c] B[q, c] over a contraction index c, with p the
 // contiguous index of the output matrix and q its row: the MFMA's D registers of a lane then run

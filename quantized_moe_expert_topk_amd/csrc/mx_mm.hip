@@ -10,7 +10,8 @@
 // instructions and their LDS reads alone 37, the two without LDS reads 49: the clock falls with what the matrix cores spend
 // (operands held in registers reach 6.6 PFLOP/s, 42 us), and loads into LDS and reads from it share its port.  65536 rows of
 // 256 experts, 1024 x 2048 (490 MB): 129; loads alone 83, of one tile only 55, without stores 100: memory, then the stores.
-// Choices, with what they measured at 8192 x 4096 x 4096 unless another size is given:
+// Choices, with what they measured at 8192 x 4096 x 4096 unless another size is given (8 experts: 4096 x 4096; each pair of
+// figures is of one run on one card, and runs differ by a few per cent):
 // - 32 x 32 x 64 instructions (mx_dev.h), a wave tile of 64 x 64: most products a byte read from LDS that leaves room for
 //   three stages; 256 x 256 tiles with two stages took as long (72, and 176 against 165 for 8 experts of 2048 rows).
 // - Four waves that only load, beside four or eight that multiply: 256 x 128 tiles 76 to 72, 8 experts of 2048 rows 184 to

@@ -29,7 +29,8 @@ def _width(codes: torch.Tensor, name: str) -> int:
 
 def moe_quantize_mx(x: torch.Tensor, slots: torch.Tensor | None = None, rows: int | None = None,
                     q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
-    """bf16 rows [T, K] to codes [M, K / 2] and scales [ceil(K / 128), M, 4].  Without ``slots`` M is T; with slots
+    """bf16 rows [T, K] to codes [M, K / 2] and scales [ceil(K / 128), M, 4]: the least power of two that leaves nothing of a
+    block above the largest code (the OCP MX conversion takes half of it for some blocks, and saturates).  Without ``slots`` M is T; with slots
     [T, k] token t goes to rows slots[t], the other rows stay as they were, and M is that of ``q`` or ``scale``, else
     ``rows``, else T * k."""
     T, K = _sizes(x, "x")
